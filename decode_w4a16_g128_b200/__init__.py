@@ -84,9 +84,18 @@ def _load() -> ctypes.CDLL:
     lib.w4a16_quantize.argtypes = [p, ctypes.c_int32, p, p, p, i64, i64, p]
     lib.w4a16_gate_up.argtypes = [p, p, p, p, p, i64, i64, i64, p]
     lib.w4a16_matmul_bits.argtypes = [p, p, p, p, p, i64, i64, i64, ctypes.c_int32, p]
+    lib.w4a16_mx_quantize.argtypes = [p, ctypes.c_int32, p, p, i64, i64, p]
+    lib.w4a16_mx_dequantize.argtypes = [p, p, p, ctypes.c_int32, i64, i64, p]
+    lib.w4a16_mx_matmul.argtypes = [p, p, p, p, i64, i64, i64, p]
+    lib.w4a16_mx_matmul_a4.argtypes = [p, p, p, p, p, i64, i64, i64, p]
+    lib.w4a16_mx_gate_up.argtypes = [p, p, p, p, i64, i64, i64, p]
+    lib.w4a16_mx_matmul_backward.argtypes = [p, p, p, p, i64, i64, i64, p]
+    lib.w4a16_mx_gate_up_backward.argtypes = [p, p, p, p, p, p, i64, i64, i64, p]
     for name in ("w4a16_matmul", "w4a16_matmul_ex", "w4a16_matmul_last_rows", "w4a16_plan",
                  "w4a16_device_status", "w4a16_last_cuda_error", "w4a16_version", "w4a16_matvec_noalloc",
-                 "w4a16_quantize", "w4a16_gate_up", "w4a16_matmul_bits"):
+                 "w4a16_quantize", "w4a16_gate_up", "w4a16_matmul_bits", "w4a16_mx_quantize", "w4a16_mx_dequantize",
+                 "w4a16_mx_matmul", "w4a16_mx_matmul_a4", "w4a16_mx_gate_up", "w4a16_mx_matmul_backward",
+                 "w4a16_mx_gate_up_backward"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -279,6 +288,186 @@ def w4a16_quantize(w, wq=None, scales=None, biases=None, stream=None):
     return wq, scales, biases
 
 
+# ---------------------------------------------------------------- MXFP4 (microscaled 4-bit float)
+#
+# wq int32/uint32 [N, K/8] codes and scales uint8 [N, K/32], as in include/w4a16.h.  Tensors are
+# contiguous and on one CUDA device, which need not be the current one; outputs that are not given
+# are allocated there.  The checks run on every call of a decode loop, so they look at each tensor
+# once and build messages only when they fail.
+
+MX_BLOCK = 32
+
+
+def _mx_fail(name, t, dtype, shape):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype and not (dtype == torch.int32 and t.dtype == torch.uint32):
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}, or is on another device than "
+                     "the first argument")
+
+
+def _mx_need(name, t, dtype, shape, device):
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        import torch
+        if not (dtype == torch.int32 and t.dtype == torch.uint32 and t.shape == shape and t.device == device
+                and t.is_contiguous()):
+            _mx_fail(name, t, dtype, shape)
+
+
+def _mx_rows(name, t, dtypes):
+    """(rows, columns, device) of a 2-D CUDA tensor whose columns are a whole number of blocks or
+    are checked by the caller."""
+    if t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}")
+    return t.shape[0], t.shape[1], t.device
+
+
+def _mx_out(name, t, dtype, shape, device, stream):
+    """A given output, checked, or a new one; new memory that another stream than its own will
+    write is recorded on that stream."""
+    import torch
+    if t is not None:
+        _mx_need(name, t, dtype, shape, device)
+        return t
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device))
+    return t
+
+
+def _mx_call(name, device, stream, *args):
+    """Runs a C entry point on `device` (made current for the call) and its stream."""
+    import torch
+    index = device.index
+    fn = getattr(lib, name)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != OK:
+        raise W4A16Error(status, name)
+
+
+def _mx_weights(wq, scales, K, device):
+    """N of stored weights [N, K/8], [N, K/32]."""
+    import torch
+    if K % MX_BLOCK:
+        raise W4A16Error(ERR_UNSUPPORTED, f"rows of {K} values: K must be a multiple of {MX_BLOCK}")
+    if wq.dim() != 2:
+        raise ValueError("wq must be 2-D")
+    N = wq.shape[0]
+    _mx_need("wq", wq, torch.int32, (N, K // 8), device)
+    _mx_need("scales", scales, torch.uint8, (N, K // MX_BLOCK), device)
+    return N
+
+
+def w4a16_mx_quantize(w, wq=None, scales=None, stream=None):
+    """Quantise w [N, K] (float32 or bfloat16: weights, or activations for w4a16_mx_matmul_a4) to
+    MXFP4: returns (wq int32 [N, K/8], scales uint8 [N, K/32])."""
+    import torch
+    N, K, device = _mx_rows("w", w, (torch.float32, torch.bfloat16))
+    if K % MX_BLOCK:
+        raise W4A16Error(ERR_UNSUPPORTED, "w4a16_mx_quantize")
+    wq = _mx_out("wq", wq, torch.int32, (N, K // 8), device, stream)
+    scales = _mx_out("scales", scales, torch.uint8, (N, K // MX_BLOCK), device, stream)
+    _mx_call("w4a16_mx_quantize", device, stream, w.data_ptr(), DTYPE_F32 if w.dtype == torch.float32 else DTYPE_BF16,
+             wq.data_ptr(), scales.data_ptr(), N, K)
+    return wq, scales
+
+
+def w4a16_mx_dequantize(wq, scales, w=None, dtype=None, stream=None):
+    """The values of stored codes [N, K], bfloat16 (default) or float32; both hold them exactly."""
+    import torch
+    N, words, device = _mx_rows("wq", wq, (torch.int32, torch.uint32))
+    K = words * 8
+    _mx_weights(wq, scales, K, device)
+    dtype = (torch.bfloat16 if w is None else w.dtype) if dtype is None else dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("values come in float32 or bfloat16")
+    w = _mx_out("w", w, dtype, (N, K), device, stream)
+    _mx_call("w4a16_mx_dequantize", device, stream, wq.data_ptr(), scales.data_ptr(), w.data_ptr(),
+             DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16, N, K)
+    return w
+
+
+def w4a16_mx_matmul(x, wq, scales, y=None, stream=None):
+    """y [M, N] = x . W^T for W in MXFP4; x and y bfloat16, any M."""
+    import torch
+    M, K, device = _mx_rows("x", x, (torch.bfloat16,))
+    N = _mx_weights(wq, scales, K, device)
+    y = _mx_out("y", y, torch.bfloat16, (M, N), device, stream)
+    _mx_call("w4a16_mx_matmul", device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K)
+    return y
+
+
+def w4a16_mx_matmul_a4(xq, xscales, wq, scales, y=None, stream=None):
+    """y [M, N] = X . W^T with both operands in MXFP4 (X from w4a16_mx_quantize of the activations)."""
+    import torch
+    M, words, device = _mx_rows("xq", xq, (torch.int32, torch.uint32))
+    K = words * 8
+    _mx_weights(xq, xscales, K, device)
+    N = _mx_weights(wq, scales, K, device)
+    y = _mx_out("y", y, torch.bfloat16, (M, N), device, stream)
+    _mx_call("w4a16_mx_matmul_a4", device, stream, xq.data_ptr(), xscales.data_ptr(), wq.data_ptr(), scales.data_ptr(),
+             y.data_ptr(), M, N, K)
+    return y
+
+
+def w4a16_mx_gate_up(x, wq, scales, h=None, stream=None):
+    """Gated block, any M: h [M, N2] = bf16(silu(x . gate^T) * (x . up^T)), the two layers' rows
+    interleaved in blocks of 8 (interleave_gate_up) in wq and scales (2 N2 rows)."""
+    import torch
+    M, K, device = _mx_rows("x", x, (torch.bfloat16,))
+    N = _mx_weights(wq, scales, K, device)
+    if N % 16:
+        raise ValueError("the interleaved gate/up rows come in blocks of 16")
+    h = _mx_out("h", h, torch.bfloat16, (M, N // 2), device, stream)
+    _mx_call("w4a16_mx_gate_up", device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), h.data_ptr(), M, N // 2, K)
+    return h
+
+
+def w4a16_mx_matmul_backward(dy, wq, scales, dx=None, stream=None):
+    """The input's gradient of w4a16_mx_matmul: dx [M, K] = dy [M, N] . W; N a multiple of 8."""
+    import torch
+    M, N, device = _mx_rows("dy", dy, (torch.bfloat16,))
+    if wq.dim() != 2:
+        raise ValueError("wq must be 2-D")
+    K = wq.shape[1] * 8
+    if _mx_weights(wq, scales, K, device) != N:
+        raise ValueError(f"dy has {N} columns, W {wq.shape[0]} rows")
+    dx = _mx_out("dx", dx, torch.bfloat16, (M, K), device, stream)
+    _mx_call("w4a16_mx_matmul_backward", device, stream, dy.data_ptr(), wq.data_ptr(), scales.data_ptr(), dx.data_ptr(),
+             M, N, K)
+    return dx
+
+
+def w4a16_mx_gate_up_backward(x, wq, scales, dh, dx=None, dgu=None, stream=None):
+    """Backward pass of w4a16_mx_gate_up from x and dh [M, N2]: returns (dx [M, K], dgu [M, 2 N2]),
+    dgu the gradients of both projections' outputs with columns interleaved like the rows of W."""
+    import torch
+    M, K, device = _mx_rows("x", x, (torch.bfloat16,))
+    N = _mx_weights(wq, scales, K, device)
+    if N % 16:
+        raise ValueError("the interleaved gate/up rows come in blocks of 16")
+    _mx_need("dh", dh, torch.bfloat16, (M, N // 2), device)
+    dx = _mx_out("dx", dx, torch.bfloat16, (M, K), device, stream)
+    dgu = _mx_out("dgu", dgu, torch.bfloat16, (M, N), device, stream)
+    _mx_call("w4a16_mx_gate_up_backward", device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), dh.data_ptr(),
+             dgu.data_ptr(), dx.data_ptr(), M, N // 2, K)
+    return dx, dgu
+
+
 def w4a16_plan(M: int, N: int, K: int, path=PATH_AUTO, splits=0, workers=0, sm_count=0, row_blocks=0) -> dict:
     opt = make_options(path, splits, workers, sm_count, 0, row_blocks)
     info = PlanInfo()
@@ -307,6 +496,8 @@ __all__ = [
     "w4a16_matmul", "w4a16_matmul_ex", "w4a16_matmul_last_rows", "w4a16_plan", "w4a16_device_status",
     "w4a16_release", "w4a16_version", "w4a16_streamk_owner", "w4a16_matvec_noalloc", "w4a16_quantize",
     "w4a16_gate_up", "interleave_gate_up", "w4a16_matmul_bits",
+    "w4a16_mx_quantize", "w4a16_mx_dequantize", "w4a16_mx_matmul", "w4a16_mx_matmul_a4", "w4a16_mx_gate_up",
+    "w4a16_mx_matmul_backward", "w4a16_mx_gate_up_backward",
     "status_string", "W4A16Error", "Options",
     "PlanInfo", "make_options", "lib", "LIBRARY_PATH",
 ]

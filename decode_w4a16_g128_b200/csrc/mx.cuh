@@ -1,0 +1,177 @@
+// mx.cuh - the microscaled 4-bit format (MXFP4): conversion helpers, the quantiser and its inverse.
+//
+// A row of K values is cut into blocks of 32; a block holds one scale byte e (the factor
+// 2^(e - 127); 255 marks a block that is not a number) and 32 codes of 4 bits: sign, two exponent
+// bits, one mantissa bit, standing for 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.  Eight codes a
+// word, the lowest k in the lowest bits, so codes are uint32 [rows, K/8], scales uint8 [rows, K/32].
+#pragma once
+
+#include "ptx.cuh"
+
+namespace w4a16 {
+namespace mx {
+
+constexpr int kBlock = 32;              // values of one scale
+constexpr uint32_t kScaleNan = 255;     // scale byte of a block that is not a number
+
+// The factor 2^(e - 127) of a scale byte, in FP32 (e = 0 is the subnormal 2^-127).
+__device__ __forceinline__ float scale_f32(uint32_t e) {
+    const uint32_t b = e == 0 ? 0x00400000u : (e == kScaleNan ? 0x7FC00000u : e << 23);
+    return __uint_as_float(b);
+}
+
+// Code -> value in FP32: exponent and mantissa bits moved under an exponent that is 126 too low
+// (code 1, the format's subnormal, lands on FP32's own subnormals), then times 2^126: exact.
+__device__ __forceinline__ float code_f32(uint32_t c) {
+    return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * __uint_as_float(253u << 23);
+}
+
+// ------------------------------------------------------------------ quantiser
+//
+// Per block: top = the largest magnitude, e = max(0, floor(log2 top) - 2 + 127), so that top lands in
+// [4, 8); code = v 2^(127 - e) rounded to the nearest value, ties to even, above 6 down to 6.  The
+// factor is a power of two and every input that a code other than 0 can come from stays exact under
+// it, so cvt.rn.satfinite.e2m1x2 rounds the true quotient once: the result is the same bit for bit
+// as a sequential CPU computation.  A block that holds an infinity or a NaN becomes e = 255, codes 0.
+//
+// Bound: HBM (4 or 2 bytes read and 0.53 written a value).  Blocks lie back to back over rows, so the
+// kernel is one-dimensional: four lanes a block, eight values a lane, the maximum in two shuffles; a
+// warp's eight code words of a step leave as 128 contiguous bytes.
+
+constexpr int kQThreads = 256;
+constexpr int kQUnroll = 4;
+
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *w, long long word, float (&v)[8]) {
+    if constexpr (BF16) {
+        const uint4 a = ldg_v4(static_cast<const uint4 *>(w) + word);
+        v[0] = bf16_lo_to_f32(a.x); v[1] = bf16_hi_to_f32(a.x);
+        v[2] = bf16_lo_to_f32(a.y); v[3] = bf16_hi_to_f32(a.y);
+        v[4] = bf16_lo_to_f32(a.z); v[5] = bf16_hi_to_f32(a.z);
+        v[6] = bf16_lo_to_f32(a.w); v[7] = bf16_hi_to_f32(a.w);
+    } else {
+        const uint4 *p = static_cast<const uint4 *>(w) + 2 * word;
+        const uint4 a = ldg_v4(p), b = ldg_v4(p + 1);
+        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+        v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+        v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    }
+}
+
+// words: code words in all (a multiple of 4).
+template <bool BF16>
+__global__ void __launch_bounds__(kQThreads) quantize_kernel(const void *w, uint32_t *wq, uint8_t *scales,
+                                                             long long words) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long stride = static_cast<long long>(gridDim.x) * kQThreads * kQUnroll;
+    for (long long base = (static_cast<long long>(blockIdx.x) * kQUnroll) * kQThreads + threadIdx.x;
+         base - threadIdx.x < words; base += stride) {
+        float v[kQUnroll][8];
+#pragma unroll
+        for (int u = 0; u < kQUnroll; ++u) {
+            const long long i = base + u * kQThreads;
+            if (i < words) {
+                load8<BF16>(w, i, v[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kQUnroll; ++u) {
+            const long long i = base + u * kQThreads;
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[u][j]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const uint32_t ex = top >> 23;
+            uint32_t e = ex > 2 ? ex - 2 : 0;
+            const float f = __uint_as_float((254u - e) << 23);     // 2^(127 - e)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[u][j] *= f;
+            uint32_t c = e2m1x8(v[u]);
+            if (ex == 255) {
+                c = 0;
+                e = kScaleNan;
+            }
+            if (i < words) {
+                wq[i] = c;
+                if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(e);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ values of stored codes
+//
+// Every value is exact in BF16 (two significant bits; 2^-128 is one of its subnormals) unless it
+// is beyond FP32's range too, where it becomes an infinity.  Bound: HBM.
+
+template <bool BF16>
+__global__ void __launch_bounds__(kQThreads) dequantize_kernel(const uint32_t *wq, const uint8_t *scales, void *w,
+                                                               long long words) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long stride = static_cast<long long>(gridDim.x) * kQThreads * kQUnroll;
+    for (long long base = (static_cast<long long>(blockIdx.x) * kQUnroll) * kQThreads + threadIdx.x; base < words;
+         base += stride) {
+        uint32_t c[kQUnroll], e[kQUnroll];
+#pragma unroll
+        for (int u = 0; u < kQUnroll; ++u) {
+            const long long i = base + u * kQThreads;
+            c[u] = i < words ? __ldcs(wq + i) : 0u;
+            e[u] = i < words ? scales[i >> 2] : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kQUnroll; ++u) {
+            const long long i = base + u * kQThreads;
+            if (i >= words) break;
+            const float s = scale_f32(e[u]);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = code_f32(c[u] >> (4 * j)) * s;
+            if constexpr (BF16) {
+                uint4 o;
+                o.x = pack_bf16x2(v[0], v[1]);
+                o.y = pack_bf16x2(v[2], v[3]);
+                o.z = pack_bf16x2(v[4], v[5]);
+                o.w = pack_bf16x2(v[6], v[7]);
+                static_cast<uint4 *>(w)[i] = o;
+            } else {
+                float4 *o = static_cast<float4 *>(w) + 2 * i;
+                o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the gated block's scalar parts
+
+// silu(g) u and its derivatives, from FP32 sums: silu(g) = g s, s = 1 / (1 + e^-g).  A large
+// negative g gives s = 0 (e^-g is an infinity) and finite results; infinite sums follow the formulas.
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
+__device__ __forceinline__ void gated_backward(float g, float u, float dh, float &dg, float &du) {
+    const float s = 1.f / (1.f + expf(-g));
+    dg = dh * u * (s * (1.f + g * (1.f - s)));
+    du = dh * (g * s);
+}
+
+}  // namespace mx
+}  // namespace w4a16

@@ -1,0 +1,235 @@
+// mx_entry.cuh - host side of the MXFP4 entry points declared in include/w4a16.h: argument checks
+// and launches.  Included by w4a16.cu, whose device set-up and helpers it uses.  None of these calls
+// allocates or keeps a workspace, so a captured call needs no warm-up and replays share nothing.
+#pragma once
+
+#include "mx.cuh"
+#include "mx_simple.cuh"
+
+namespace w4a16 {
+namespace {
+
+constexpr int64_t kSizeLimit = int64_t(1) << 31;
+
+struct Span {
+    const void *p;
+    size_t bytes;
+    bool aligned = true;   // false: any address (scale bytes)
+};
+
+// Every buffer present and aligned, no output on top of another buffer.  The first `outputs`
+// spans are written.
+int check_buffers(const Span *s, int n, int outputs) {
+    for (int i = 0; i < n; ++i)
+        if (!s[i].p && s[i].bytes) return W4A16_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (s[i].aligned && s[i].bytes && !aligned16(s[i].p)) return W4A16_ERR_MISALIGNED;
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (s[i].bytes && s[j].bytes && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return W4A16_ERR_INVALID_ARG;
+    return W4A16_OK;
+}
+
+int mx_sizes(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0) return W4A16_ERR_INVALID_ARG;
+    if (K % mx::kBlock != 0 || M >= kSizeLimit || N >= kSizeLimit || K >= kSizeLimit) return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+
+int mx_device(DeviceInfo **d) {
+    int dev = 0;
+    const int rc = current_device(&dev);
+    return rc ? rc : device_setup(dev, d);
+}
+
+int zero_fill(void *p, size_t bytes, void *stream) {
+    const cudaError_t e = cudaMemsetAsync(p, 0, bytes, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? W4A16_OK : cuda_fail(e);
+}
+
+// A launch with the programmatic-dependent-launch attribute (every kernel here waits for the
+// preceding one before its first access).
+template <typename... KArgs, typename... Args>
+int mx_launch(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, void *stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? W4A16_OK : cuda_fail(e);
+}
+
+int mx_simple(const mxs::Params &p, bool a4, bool backward, void *stream) {
+    const int64_t gx = (p.J + mxs::kTile - 1) / mxs::kTile, gy = (p.M + mxs::kTile - 1) / mxs::kTile;
+    if (gy > 65535) return W4A16_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1);
+    if (a4) return mx_launch(mxs::product_kernel<true, false>, grid, mxs::kThreads, 0, stream, p);
+    if (backward) return mx_launch(mxs::product_kernel<false, true>, grid, mxs::kThreads, 0, stream, p);
+    return mx_launch(mxs::product_kernel<false, false>, grid, mxs::kThreads, 0, stream, p);
+}
+
+mxs::Params mx_params(const void *a, const uint32_t *aq, const uint8_t *as, const uint32_t *wq, const uint8_t *ws,
+                      const void *dh, void *out, int64_t M, int64_t J, int64_t C, int64_t K, int epilogue) {
+    mxs::Params p;
+    p.a = static_cast<const uint16_t *>(a);
+    p.aq = aq;
+    p.as = as;
+    p.wq = wq;
+    p.ws = ws;
+    p.dh = static_cast<const uint16_t *>(dh);
+    p.out = static_cast<uint16_t *>(out);
+    p.M = static_cast<int>(M);
+    p.J = static_cast<int>(J);
+    p.C = static_cast<int>(C);
+    p.K = static_cast<int>(K);
+    p.epilogue = epilogue;
+    return p;
+}
+
+unsigned stream_grid(int64_t words, int sms) {
+    const int64_t per = int64_t(mx::kQThreads) * mx::kQUnroll;
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((words + per - 1) / per, int64_t(sms) * 8)));
+}
+
+}  // namespace
+}  // namespace w4a16
+
+extern "C" {
+
+int w4a16_mx_quantize(const void *w, int32_t w_dtype, uint32_t *wq, uint8_t *scales, int64_t N, int64_t K,
+                      void *stream) {
+    if (w_dtype != W4A16_DTYPE_F32 && w_dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    int rc = mx_sizes(0, N, K);
+    if (rc || N == 0 || K == 0) return rc;
+    const size_t n = size_t(N) * K;
+    const Span s[3] = {{wq, n / 2}, {scales, n / 32, false}, {w, n * (w_dtype == W4A16_DTYPE_F32 ? 4 : 2)}};
+    rc = check_buffers(s, 3, 2);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceInfo *d = nullptr;
+    rc = mx_device(&d);
+    if (rc) return rc;
+    const long long words = N * (K / 8);
+    const dim3 grid(stream_grid(words, d->sms), 1, 1);
+    if (w_dtype == W4A16_DTYPE_BF16)
+        return mx_launch(mx::quantize_kernel<true>, grid, mx::kQThreads, 0, stream, w, wq, scales, words);
+    return mx_launch(mx::quantize_kernel<false>, grid, mx::kQThreads, 0, stream, w, wq, scales, words);
+}
+
+int w4a16_mx_dequantize(const uint32_t *wq, const uint8_t *scales, void *w, int32_t w_dtype, int64_t N, int64_t K,
+                        void *stream) {
+    if (w_dtype != W4A16_DTYPE_F32 && w_dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    int rc = mx_sizes(0, N, K);
+    if (rc || N == 0 || K == 0) return rc;
+    const size_t n = size_t(N) * K;
+    const Span s[3] = {{w, n * (w_dtype == W4A16_DTYPE_F32 ? 4 : 2)}, {wq, n / 2}, {scales, n / 32, false}};
+    rc = check_buffers(s, 3, 1);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceInfo *d = nullptr;
+    rc = mx_device(&d);
+    if (rc) return rc;
+    const long long words = N * (K / 8);
+    const dim3 grid(stream_grid(words, d->sms), 1, 1);
+    if (w_dtype == W4A16_DTYPE_BF16)
+        return mx_launch(mx::dequantize_kernel<true>, grid, mx::kQThreads, 0, stream, wq, scales, w, words);
+    return mx_launch(mx::dequantize_kernel<false>, grid, mx::kQThreads, 0, stream, wq, scales, w, words);
+}
+
+int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, void *y, int64_t M, int64_t N, int64_t K,
+                    void *stream) {
+    int rc = mx_sizes(M, N, K);
+    if (rc || M == 0 || N == 0) return rc;
+    const size_t nw = size_t(N) * K;
+    const Span s[4] = {{y, size_t(M) * N * 2}, {x, size_t(M) * K * 2}, {wq, nw / 2}, {scales, nw / 32, false}};
+    rc = check_buffers(s, 4, 1);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceInfo *d = nullptr;
+    rc = mx_device(&d);
+    if (rc) return rc;
+    if (K == 0) return zero_fill(y, s[0].bytes, stream);   // an empty sum
+    return mx_simple(mx_params(x, nullptr, nullptr, wq, scales, nullptr, y, M, N, K, K, mxs::kPlain), false, false, stream);
+}
+
+int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_t *wq, const uint8_t *scales, void *y,
+                       int64_t M, int64_t N, int64_t K, void *stream) {
+    int rc = mx_sizes(M, N, K);
+    if (rc || M == 0 || N == 0) return rc;
+    const size_t nx = size_t(M) * K, nw = size_t(N) * K;
+    const Span s[5] = {{y, size_t(M) * N * 2}, {xq, nx / 2}, {xscales, nx / 32, false}, {wq, nw / 2}, {scales, nw / 32, false}};
+    rc = check_buffers(s, 5, 1);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceInfo *d = nullptr;
+    rc = mx_device(&d);
+    if (rc) return rc;
+    if (K == 0) return zero_fill(y, s[0].bytes, stream);
+    return mx_simple(mx_params(nullptr, xq, xscales, wq, scales, nullptr, y, M, N, K, K, mxs::kPlain), true, false, stream);
+}
+
+int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, void *h, int64_t M, int64_t N2, int64_t K,
+                     void *stream) {
+    int rc = mx_sizes(M, N2, K);
+    if (rc) return rc;
+    if (N2 % 8 != 0 || N2 >= kSizeLimit / 2) return W4A16_ERR_UNSUPPORTED;
+    if (M == 0 || N2 == 0) return W4A16_OK;
+    const size_t nw = size_t(N2) * 2 * K;
+    const Span s[4] = {{h, size_t(M) * N2 * 2}, {x, size_t(M) * K * 2}, {wq, nw / 2}, {scales, nw / 32, false}};
+    rc = check_buffers(s, 4, 1);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceInfo *d = nullptr;
+    rc = mx_device(&d);
+    if (rc) return rc;
+    if (K == 0) return zero_fill(h, s[0].bytes, stream);   // silu(0) 0 = +0
+    return mx_simple(mx_params(x, nullptr, nullptr, wq, scales, nullptr, h, M, 2 * N2, K, K, mxs::kGated), false, false, stream);
+}
+
+int w4a16_mx_matmul_backward(const void *dy, const uint32_t *wq, const uint8_t *scales, void *dx, int64_t M, int64_t N,
+                             int64_t K, void *stream) {
+    int rc = mx_sizes(M, N, K);
+    if (rc) return rc;
+    if (N % 8 != 0) return W4A16_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return W4A16_OK;
+    const size_t nw = size_t(N) * K;
+    const Span s[4] = {{dx, size_t(M) * K * 2}, {dy, size_t(M) * N * 2}, {wq, nw / 2}, {scales, nw / 32, false}};
+    rc = check_buffers(s, 4, 1);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceInfo *d = nullptr;
+    rc = mx_device(&d);
+    if (rc) return rc;
+    if (N == 0) return zero_fill(dx, s[0].bytes, stream);
+    return mx_simple(mx_params(dy, nullptr, nullptr, wq, scales, nullptr, dx, M, K, N, K, mxs::kPlain), false, true, stream);
+}
+
+int w4a16_mx_gate_up_backward(const void *x, const uint32_t *wq, const uint8_t *scales, const void *dh, void *dgu,
+                              void *dx, int64_t M, int64_t N2, int64_t K, void *stream) {
+    int rc = mx_sizes(M, N2, K);
+    if (rc) return rc;
+    if (N2 % 8 != 0 || N2 >= kSizeLimit / 2) return W4A16_ERR_UNSUPPORTED;
+    if (M == 0) return W4A16_OK;
+    const size_t nw = size_t(N2) * 2 * K;
+    const Span s[6] = {{dx, size_t(M) * K * 2},  {dgu, size_t(M) * N2 * 4}, {x, size_t(M) * K * 2},
+                       {dh, size_t(M) * N2 * 2}, {wq, nw / 2},              {scales, nw / 32, false}};
+    rc = check_buffers(s, 6, 2);
+    if (rc) return rc;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceInfo *d = nullptr;
+    rc = mx_device(&d);
+    if (rc) return rc;
+    if (N2 == 0) return K == 0 ? W4A16_OK : zero_fill(dx, s[0].bytes, stream);
+    if (K == 0) return zero_fill(dgu, s[1].bytes, stream);   // g = u = 0: both gradients are 0
+    rc = mx_simple(mx_params(x, nullptr, nullptr, wq, scales, dh, dgu, M, 2 * N2, K, K, mxs::kGatedBackward), false, false, stream);
+    if (rc) return rc;
+    return mx_simple(mx_params(dgu, nullptr, nullptr, wq, scales, nullptr, dx, M, K, 2 * N2, K, mxs::kPlain), false, true, stream);
+}
+
+}  // extern "C"

@@ -1135,3 +1135,5 @@ int w4a16_quantize(const void *w, int32_t w_dtype, uint32_t *wq, void *scales, v
 }
 
 }  // extern "C"
+
+#include "mx_entry.cuh"   // the MXFP4 entry points

@@ -309,6 +309,82 @@ int w4a16_matmul_bits(const void *x, const uint32_t *wq, const void *scales,
                       const void *biases, void *y, int64_t M, int64_t N, int64_t K,
                       int32_t bits, void *stream);
 
+/*
+ * Microscaled 4-bit floating point (MXFP4): the quantiser, products and a gated feed-forward block.
+ *
+ * Format: blocks of 32 values along K share one scale byte e, the factor 2^(e - 127) (e = 255: the
+ * block is not a number, all of its values are NaN).  A value is a 4-bit code, sign, two exponent
+ * bits and one mantissa bit: codes 0..7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, codes 8..15 for their
+ * negatives.
+ *   wq      uint32 [N, K/8]    code of w[n,k]: (wq[n*(K/8) + k/8] >> (4*(k%8))) & 15
+ *   scales  uint8  [N, K/32]   any address; every other pointer must be 16-byte aligned
+ * Activations and gradients are BF16, row-major, contiguous.  K must be a multiple of 32 and sizes
+ * below 2^31 (W4A16_ERR_UNSUPPORTED); negative sizes, null pointers with non-empty sizes and an
+ * output that overlaps another buffer are W4A16_ERR_INVALID_ARG.  An empty output launches nothing;
+ * an empty sum is +0.  Rows behind M are neither read nor written.
+ *
+ * Numerics: every stored value is exact in BF16, every product exact in FP32; sums are FP32 (order
+ * fixed by the sizes and the device model, so results repeat bit for bit), rounded once to BF16.
+ * NaN and infinities in a row of x reach that row's outputs alone; a NaN block of W reaches its
+ * row's outputs alone.
+ *
+ * Execution: on `stream` of the current device, without waiting, allocating or using a library
+ * workspace: the calls may be captured without a warm-up call, and calls on different streams or
+ * replays of different graphs share nothing.
+ */
+
+/*
+ * Quantiser.  w [N, K] FP32 or BF16 (weights, or activations on their way into
+ * w4a16_mx_matmul_a4) -> codes and scales.  Per block: top = the largest magnitude,
+ * e = max(0, floor(log2(top)) + 125), code = w 2^(127 - e) rounded to the nearest value (ties to
+ * the even code; above 6: 6; the sign of a zero stays).  An all-zero block has e = 0; a block with an
+ * infinity or a NaN has e = 255 and codes 0.  Bit-identical to the same steps done one by one.
+ */
+int w4a16_mx_quantize(const void *w, int32_t w_dtype, uint32_t *wq, uint8_t *scales, int64_t N, int64_t K,
+                      void *stream);
+
+/* The values of stored codes: w [N, K] FP32 or BF16 (both exact), written. */
+int w4a16_mx_dequantize(const uint32_t *wq, const uint8_t *scales, void *w, int32_t w_dtype, int64_t N,
+                        int64_t K, void *stream);
+
+/* y [M, N] = x [M, K] . W^T, W in the format above.  Any M: one token to a long prompt. */
+int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, void *y, int64_t M, int64_t N,
+                    int64_t K, void *stream);
+
+/*
+ * The same product with x in the format too (from w4a16_mx_quantize): xq uint32 [M, K/8], xscales
+ * uint8 [M, K/32].  Both operands stay in 4 bits up to the tensor cores.
+ */
+int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_t *wq, const uint8_t *scales,
+                       void *y, int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * Gated feed-forward block: h [M, N2] = bf16(silu(g) * u), g = x . Wg^T, u = x . Wu^T in FP32.  The
+ * rows of Wg and Wu are interleaved in blocks of 8 as in w4a16_gate_up: wq [2 N2, K/8], scales
+ * [2 N2, K/32].  N2 % 8 == 0 (else W4A16_ERR_UNSUPPORTED); any M.
+ */
+int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, void *h, int64_t M, int64_t N2,
+                     int64_t K, void *stream);
+
+/*
+ * The input's gradient of w4a16_mx_matmul: dx [M, K] = dy [M, N] . W.  N % 8 == 0 (else
+ * W4A16_ERR_UNSUPPORTED).  The codes are not differentiable: x is the only input with a gradient.
+ */
+int w4a16_mx_matmul_backward(const void *dy, const uint32_t *wq, const uint8_t *scales, void *dx, int64_t M,
+                             int64_t N, int64_t K, void *stream);
+
+/*
+ * Backward pass of w4a16_mx_gate_up, from x and dh [M, N2] alone (g and u are computed again, so the
+ * forward pass keeps nothing):
+ *   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s,  s = 1 / (1 + exp(-g))      (FP32)
+ *   dgu [M, 2 N2] = bf16 of dg and du, columns interleaved in blocks of 8 like the rows of W
+ *   dx [M, K] = dgu . W
+ * dgu and dx are both written; dgu is rounded to BF16 before the second product (the tensor cores'
+ * operand type), and is what the gradients of adapters beside the projections are made from.
+ */
+int w4a16_mx_gate_up_backward(const void *x, const uint32_t *wq, const uint8_t *scales, const void *dh,
+                              void *dgu, void *dx, int64_t M, int64_t N2, int64_t K, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

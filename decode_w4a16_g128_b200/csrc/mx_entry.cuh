@@ -4,6 +4,7 @@
 #pragma once
 
 #include "mx.cuh"
+#include "mx_gemm.cuh"
 #include "mx_simple.cuh"
 
 namespace w4a16 {
@@ -38,8 +39,15 @@ int mx_sizes(int64_t M, int64_t N, int64_t K) {
 
 int mx_device(DeviceInfo **d) {
     int dev = 0;
-    const int rc = current_device(&dev);
-    return rc ? rc : device_setup(dev, d);
+    int rc = current_device(&dev);
+    if (!rc) rc = device_setup(dev, d);
+    if (rc || (*d)->mx_ready) return rc;
+    cudaError_t e = cudaFuncSetAttribute(mxg::gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(mxg::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
+    if (e != cudaSuccess) return cuda_fail(e);
+    (*d)->mx_ready = true;
+    return W4A16_OK;
 }
 
 int zero_fill(void *p, size_t bytes, void *stream) {
@@ -90,6 +98,75 @@ mxs::Params mx_params(const void *a, const uint32_t *aq, const uint8_t *as, cons
     p.K = static_cast<int>(K);
     p.epilogue = epilogue;
     return p;
+}
+
+// Outputs of a CTA pair: the width with the least estimated time, rounds of the persistent grid times
+// the SM cycles of a stage (four MMAs of 256 rows, or the expanding of half of the outputs' codes).
+int mx_gemm_width(int64_t M, int64_t J, bool backward, int pairs) {
+    const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows);
+    int best = 0;
+    int64_t cost = 0;
+    for (int bn = 64; bn <= (backward ? 320 : 256); bn += backward ? 64 : 32) {
+        const int64_t tiles = tm * ((J + bn - 1) / bn), rounds = (tiles + pairs - 1) / pairs;
+        const int64_t mma = bn <= 256 ? std::max(bn / 2, 52) : 128 + std::max((bn - 256) / 2, 52);
+        const int64_t c = rounds * std::max<int64_t>(4 * mma, 256);
+        if (!best || c <= cost) {
+            best = bn;
+            cost = c;
+        }
+    }
+    return best;
+}
+
+// D = A . W^T (forward) or A . W (backward) on the tensor cores: A bf16 [M, C], J outputs.
+int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws, const void *dh, void *out, int64_t M,
+            int64_t J, int64_t C, int64_t N, int64_t K, bool backward, int epilogue, void *stream) {
+    const int pairs = d->sms / 2;
+    mxg::Params p;
+    p.ws = ws;
+    p.dh = static_cast<const uint16_t *>(dh);
+    p.out = static_cast<uint16_t *>(out);
+    p.M = static_cast<int>(M);
+    p.J = static_cast<int>(J);
+    p.C = static_cast<int>(C);
+    p.ks = static_cast<int>(K / mx::kBlock);
+    p.bn = mx_gemm_width(M, J, backward, pairs);
+    const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows), tiles = tm * ((J + p.bn - 1) / p.bn);
+    if (tiles >= kSizeLimit) return W4A16_ERR_UNSUPPORTED;
+    p.tiles_m = static_cast<int>(tm);
+    p.tiles = static_cast<int>(tiles);
+    const int half = p.bn / 2;
+    p.b_bytes = backward ? (half + 63) / 64 * 8192 : half * 128;
+    p.w_bytes = 32 * half;
+    p.w_pitch = backward ? half / 2 : 32;
+    // codes tile: rows of 32 and 64 bytes are swizzled by the copy (else neighbouring rows' 16-byte
+    // chunks would share banks); 16-byte chunks at a pitch of 48 or 80 bytes spread by themselves
+    CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE;
+    p.w_swz_shift = p.w_swz_mask = 0;
+    if (p.w_pitch == 32) {
+        swz = CU_TENSOR_MAP_SWIZZLE_32B;
+        p.w_swz_shift = 2;
+        p.w_swz_mask = 1;
+    } else if (p.w_pitch == 64) {
+        swz = CU_TENSOR_MAP_SWIZZLE_64B;
+        p.w_swz_shift = 1;
+        p.w_swz_mask = 3;
+    }
+    p.stages = mxg::kMaxStages;
+    while (mxg::smem_bytes(p.stages, p.b_bytes, p.w_bytes) > mxg::kSmemBudget) --p.stages;
+    p.epilogue = epilogue;
+    const int smem = mxg::smem_bytes(p.stages, p.b_bytes, p.w_bytes);
+
+    CUtensorMap tx, tw;
+    int rc = encode_2d(d, &tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a, C, M, C * 2, mxg::kStep, mxg::kRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+    rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : mxg::kStep / 8,
+                   backward ? mxg::kStep : half, swz);
+    if (rc) return rc;
+    const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)), 1, 1);
+    const auto kernel = backward ? mxg::gemm_kernel<true> : mxg::gemm_kernel<false>;
+    return mx_launch(kernel, grid, mxg::kThreads, smem, stream, tx, tw, p);
 }
 
 unsigned stream_grid(int64_t words, int sms) {
@@ -155,7 +232,7 @@ int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, vo
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(y, s[0].bytes, stream);   // an empty sum
-    return mx_simple(mx_params(x, nullptr, nullptr, wq, scales, nullptr, y, M, N, K, K, mxs::kPlain), false, false, stream);
+    return mx_gemm(d, x, wq, scales, nullptr, y, M, N, K, N, K, false, mxg::kPlain, stream);
 }
 
 int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_t *wq, const uint8_t *scales, void *y,
@@ -189,7 +266,7 @@ int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, v
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(h, s[0].bytes, stream);   // silu(0) 0 = +0
-    return mx_simple(mx_params(x, nullptr, nullptr, wq, scales, nullptr, h, M, 2 * N2, K, K, mxs::kGated), false, false, stream);
+    return mx_gemm(d, x, wq, scales, nullptr, h, M, 2 * N2, K, 2 * N2, K, false, mxg::kGated, stream);
 }
 
 int w4a16_mx_matmul_backward(const void *dy, const uint32_t *wq, const uint8_t *scales, void *dx, int64_t M, int64_t N,
@@ -207,7 +284,7 @@ int w4a16_mx_matmul_backward(const void *dy, const uint32_t *wq, const uint8_t *
     rc = mx_device(&d);
     if (rc) return rc;
     if (N == 0) return zero_fill(dx, s[0].bytes, stream);
-    return mx_simple(mx_params(dy, nullptr, nullptr, wq, scales, nullptr, dx, M, K, N, K, mxs::kPlain), false, true, stream);
+    return mx_gemm(d, dy, wq, scales, nullptr, dx, M, K, N, N, K, true, mxg::kPlain, stream);
 }
 
 int w4a16_mx_gate_up_backward(const void *x, const uint32_t *wq, const uint8_t *scales, const void *dh, void *dgu,
@@ -227,9 +304,9 @@ int w4a16_mx_gate_up_backward(const void *x, const uint32_t *wq, const uint8_t *
     if (rc) return rc;
     if (N2 == 0) return K == 0 ? W4A16_OK : zero_fill(dx, s[0].bytes, stream);
     if (K == 0) return zero_fill(dgu, s[1].bytes, stream);   // g = u = 0: both gradients are 0
-    rc = mx_simple(mx_params(x, nullptr, nullptr, wq, scales, dh, dgu, M, 2 * N2, K, K, mxs::kGatedBackward), false, false, stream);
+    rc = mx_gemm(d, x, wq, scales, dh, dgu, M, 2 * N2, K, 2 * N2, K, false, mxg::kGatedBackward, stream);
     if (rc) return rc;
-    return mx_simple(mx_params(dgu, nullptr, nullptr, wq, scales, nullptr, dx, M, K, 2 * N2, K, mxs::kPlain), false, true, stream);
+    return mx_gemm(d, dgu, wq, scales, nullptr, dx, M, K, 2 * N2, 2 * N2, K, true, mxg::kPlain, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,498 @@
+// mx_gemm.cuh - tcgen05 product of BF16 rows with MXFP4 weights, by rows or by columns of W.
+//
+//   forward:  D[m, j] = sum_k x[m, k] W[j, k]        (j = n: outputs;  contraction over k)
+//   backward: D[m, j] = sum_n dy[m, n] W[n, j]       (j = k: the input's gradient)
+//
+// Mathematics: a stored value code 2^(e - 127) has two significant bits, so it is exact in BF16 (the
+// scale is applied before the product, no factor is left for the accumulator) and the tensor cores'
+// products are exact in FP32; the sum over all of the contraction stays in tensor memory.
+//
+// A CTA pair (cta_group::2) computes 256 rows x BN outputs, K = 64 of the contraction a stage:
+//   A  128 rows x 64 of x per CTA, by TMA, K-major, 128-byte swizzle;
+//   B  each CTA expands its BN / 2 outputs' codes into BF16 in shared memory.  Forward: [output][64 k],
+//      K-major.  Backward: the stored rows run along the outputs, so the tile is kept as stored,
+//      [64 n][64 outputs] per group of 64 outputs, MN-major: the transposition is the descriptor's.
+//      BN > 256 (backward) is a second MMA over the outputs behind the first 128 of each CTA.
+// Accumulators fill tensor memory: two of BN <= 256 columns (the epilogue of a tile runs under the
+// next tile's main loop), or one wider.  The grid is persistent; the host picks BN for the fewest
+// column-rounds (see mx_entry.cuh).
+//
+// Roles (512 threads): warp 0 x by TMA, warp 1 MMA issue (leader) and tensor memory, warp 2 codes by
+// TMA, warp 3 of the peer forwards "expanded" to the leader, warps 4-7 epilogue, warps 8-15 expand
+// codes.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's eight expanding warps, the
+// peer's forwarder), empty[s] (both CTAs; the stage's MMAs completed), exp[s] (peer: its eight
+// expanding warps), w_full / w_empty (codes ring), acc_full / acc_empty (accumulators).
+#pragma once
+
+#include "mx.cuh"
+
+namespace w4a16 {
+namespace mxg {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 128;               // x rows of a CTA
+constexpr int kStep = 64;                // contraction of a stage
+constexpr int kABytes = kRows * kStep * 2;
+constexpr int kMaxStages = 8;
+constexpr int kWSlots = 8;
+constexpr int kDeqWarps = 8, kDeqThreads = 32 * kDeqWarps, kEpiWarps = 4;
+constexpr int kTmemCols = 512;
+constexpr int kMaxBN = 320;              // outputs of a pair (forward: 256)
+constexpr int kBarBytes = 512;
+constexpr int kSmemBudget = 227 * 1024;
+constexpr int kMaxTasks = 2;             // blocks of 32 codes of a thread and stage
+
+enum Epilogue { kPlain = 0, kGated = 1, kGatedBackward = 2 };
+
+struct Params {
+    const uint8_t *ws;        // scales [N, K/32]
+    const uint16_t *dh;       // bf16 [M, J/2] (kGatedBackward)
+    uint16_t *out;            // bf16 [M, J], or [M, J/2] (kGated)
+    int M, J, C;              // rows, outputs, contraction
+    int ks;                   // scale bytes of a row of W (K / 32)
+    int bn;                   // outputs of a pair
+    int tiles_m, tiles;
+    int stages;
+    int b_bytes, w_bytes;     // B tile and codes tile of a CTA and stage
+    int w_pitch;              // bytes of a codes tile row
+    int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
+    int epilogue;
+};
+
+// Dynamic shared memory: stages x (A, B), codes ring, barriers, and slack for 1024-byte alignment.
+__host__ __device__ constexpr int smem_bytes(int stages, int b_bytes, int w_bytes) {
+    return stages * (kABytes + b_bytes) + kWSlots * w_bytes + kBarBytes + 1024;
+}
+
+// ------------------------------------------------------------------ PTX
+
+// Arrive (release, cluster scope) on an mbarrier of another CTA: what this thread has seen
+// written, through barriers too, is visible there.
+__device__ __forceinline__ void arrive_cluster_release(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Bounded wait of the MMA issuer, acquire at cluster scope (the peer's expanded codes are behind it).
+__device__ __forceinline__ bool wait_cluster_spin(uint64_t *bar, uint32_t parity) {
+    auto test = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (test()) return true;
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t spin = 1;; ++spin) {
+        if (test()) return true;
+        if ((spin & 1023u) == 0) {
+            if (status_set()) return false;
+            if (globaltimer() - t0 > kWaitTimeoutNs) {
+                record_timeout();
+                return false;
+            }
+        }
+    }
+}
+
+// D[tmem] (+)= A[smem] . B[smem] of a CTA pair, issued by the leader.
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// Descriptor of an MN-major operand, 128-byte swizzle: rows of 64 contiguous outputs (128 bytes), 8
+// rows of the contraction 1024 bytes apart (stride offset), groups of 64 outputs 8192 bytes apart
+// (leading offset).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr) {
+    uint64_t d = static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(8192 >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;
+
+// ------------------------------------------------------------------ codes to BF16
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A scale byte as up to two BF16 factors: a code's three low bits in BF16's lowest exponent bits
+// and highest mantissa bit are its magnitude times 2^-126 (code 1 as a subnormal), so the factor is
+// 2^(e - 1); above e = 128 that is beyond BF16 and the rest, 2^(e - 128), comes as a second one.
+struct Factor {
+    uint32_t f, more;          // pairs; more = 0: none
+};
+__device__ __forceinline__ Factor factor_of(uint32_t e) {
+    Factor r;
+    r.f = ((e < 128u ? e : 128u) + 126u) * 0x00800080u;
+    r.more = 0;
+    if (e > 128u) {
+        r.more = e == mx::kScaleNan ? 0x7FC07FC0u : (e - 1u) * 0x00800080u;
+    }
+    return r;
+}
+
+// Eight codes, lowest k first -> four BF16 pairs, lowest k first.  Codes 2i and 2i + 1 go to the two
+// halves of a register (the selector's sign-replicating bytes are zero there: every byte is below
+// 128), one multiplication by 2^12 + 2^6 puts the sign bit to bit 15 and the others to bits 6-8.
+__device__ __forceinline__ void expand8(uint32_t v, const Factor &s, uint32_t (&r)[4]) {
+    const uint32_t lo = v & 0x0F0F0F0Fu, hi = (v >> 4) & 0x0F0F0F0Fu;
+    r[0] = prmt(lo, hi, 0xC480u);
+    r[1] = prmt(lo, hi, 0xD591u);
+    r[2] = prmt(lo, hi, 0xE6A2u);
+    r[3] = prmt(lo, hi, 0xF7B3u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2((r[i] * 0x1040u) & 0x81C081C0u, s.f);
+    if (s.more) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], s.more);
+    }
+}
+
+// ------------------------------------------------------------------ epilogue helpers
+
+__device__ __forceinline__ void store16(uint16_t *dst, const float *v) {
+    uint4 o;
+    o.x = pack_bf16x2(v[0], v[1]);
+    o.y = pack_bf16x2(v[2], v[3]);
+    o.z = pack_bf16x2(v[4], v[5]);
+    o.w = pack_bf16x2(v[6], v[7]);
+    *reinterpret_cast<uint4 *>(dst) = o;
+}
+
+// 32 accumulator columns of one row: outputs j .. j + 31.
+__device__ __forceinline__ void write_columns(const Params &p, long long m, int j, const uint32_t (&r)[32]) {
+    if (p.epilogue == kPlain) {
+        uint16_t *dst = p.out + m * p.J + j;
+        if ((p.J & 7) == 0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * q + i]);
+                if (j + 8 * q < p.J) store16(dst + 8 * q, v);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (j + i < p.J) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[i])));
+        }
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {                 // 8 gate columns and their 8 up columns
+        if (j + 16 * q >= p.J) break;             // J is a multiple of 16
+        const long long h = m * (p.J / 2) + j / 2 + 8 * q;
+        float a[8], b[8];
+        if (p.epilogue == kGated) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                a[i] = mx::gated(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]));
+            store16(p.out + h, a);
+        } else {
+            const uint4 d = ldg_v4(p.dh + h);
+            const float dh[8] = {bf16_lo_to_f32(d.x), bf16_hi_to_f32(d.x), bf16_lo_to_f32(d.y), bf16_hi_to_f32(d.y),
+                                 bf16_lo_to_f32(d.z), bf16_hi_to_f32(d.z), bf16_lo_to_f32(d.w), bf16_hi_to_f32(d.w)};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                mx::gated_backward(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]), dh[i], a[i], b[i]);
+            uint16_t *dst = p.out + m * p.J + j + 16 * q;
+            store16(dst, a);
+            store16(dst + 8, b);
+        }
+    }
+}
+
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void advance(int n) {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// ------------------------------------------------------------------ the kernel
+
+template <bool BACKWARD>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int stages = p.stages;
+    uint8_t *sa = smem, *sb = sa + stages * kABytes, *sw = sb + stages * p.b_bytes;
+    uint64_t *ready = reinterpret_cast<uint64_t *>(sw + kWSlots * p.w_bytes);
+    uint64_t *empty = ready + kMaxStages, *expd = empty + kMaxStages;
+    uint64_t *w_full = expd + kMaxStages, *w_empty = w_full + kWSlots;
+    uint64_t *acc_full = w_empty + kWSlots, *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    static_assert((3 * kMaxStages + 2 * kWSlots + 4) * 8 + 8 <= kBarBytes, "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int steps = (p.C + kStep - 1) / kStep;
+    const int half = p.bn / 2;                       // outputs that this CTA expands
+    const int nacc = p.bn <= 256 ? 2 : 1;
+    const int pairs = static_cast<int>(gridDim.x) / 2, first = static_cast<int>(blockIdx.x) / 2;
+
+    if (threadIdx.x == 0) {
+        pdl_launch_dependents();
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&ready[i], 1 + kDeqWarps + 1);
+            mbar_init(&empty[i], 1);
+            mbar_init(&expd[i], kDeqWarps);
+        }
+        for (int i = 0; i < kWSlots; ++i) {
+            mbar_init(&w_full[i], 1);
+            mbar_init(&w_empty[i], kDeqWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 2 * kEpiWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t ready_l = dsmem_addr(smem_u32(ready), 0), acc_empty_l = dsmem_addr(smem_u32(acc_empty), 0);
+
+    if (warp == 0 && lane == 0) {
+        // ---------------------------------------------------------------- x by TMA
+        prefetch_tmap(&tm_x);
+        pdl_wait();
+        Ring st;
+        long long issued = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += pairs) {
+            const int row = (t % p.tiles_m) * 2 * kRows + static_cast<int>(rank) * kRows;
+            for (int i = 0; i < steps; ++i) {
+                if (issued >= stages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
+                if (leader) mbar_arrive_expect_tx(&ready[st.slot], 2 * kABytes);   // both CTAs' rows
+                tma_load_2d_pair(sa + st.slot * kABytes, &tm_x, ready_l + 8 * st.slot, i * kStep, row);
+                ++issued;
+                st.advance(stages);
+            }
+        }
+        // leave no copy in flight: the last stages' MMAs, which consumed them, completed
+        for (long long j = issued > stages ? issued - stages : 0; j < issued; ++j)
+            mbar_wait(&empty[j % stages], static_cast<uint32_t>((j / stages) & 1), false);
+    } else if (warp == 2 && lane == 0) {
+        // ---------------------------------------------------------------- codes by TMA
+        prefetch_tmap(&tm_w);
+        pdl_wait();
+        Ring st;
+        long long issued = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += pairs) {
+            const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
+            for (int i = 0; i < steps; ++i) {
+                if (issued >= kWSlots && !mbar_wait(&w_empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
+                mbar_arrive_expect_tx(&w_full[st.slot], p.w_bytes);
+                if constexpr (BACKWARD)
+                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], j0 / 8, i * kStep);
+                else
+                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], i * (kStep / 8), j0);
+                ++issued;
+                st.advance(kWSlots);
+            }
+        }
+        for (long long j = issued > kWSlots ? issued - kWSlots : 0; j < issued; ++j)
+            mbar_wait(&w_full[j % kWSlots], static_cast<uint32_t>((j / kWSlots) & 1), false);
+    } else if (warp == 3 && lane == 0 && !leader) {
+        // ---------------------------------------------------------------- "expanded", to the leader
+        Ring st;
+        for (int t = first; t < p.tiles; t += pairs) {
+            bool ok = true;
+            for (int i = 0; i < steps && ok; ++i) {
+                ok = mbar_wait(&expd[st.slot], st.phase);
+                if (ok) arrive_cluster_release(ready_l + 8 * st.slot);
+                st.advance(stages);
+            }
+            if (!ok) break;
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ---------------------------------------------------------------- MMA issue
+        const int n0 = p.bn < 256 ? p.bn : 256, n1 = p.bn - n0;
+        const uint32_t major = BACKWARD ? kIdescBMnMajor : 0u;
+        const uint32_t idesc0 = umma_idesc_bf16(2 * kRows, n0) | major, idesc1 = umma_idesc_bf16(2 * kRows, n1) | major;
+        Ring st, acc;
+        int done = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += pairs, ++done) {
+            // the accumulator's previous tile has been read
+            if (done >= nacc && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + acc.slot * 256;
+            for (int i = 0; i < steps; ++i) {
+                if (!wait_cluster_spin(&ready[st.slot], st.phase)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t a0 = smem_u32(sa + st.slot * kABytes), b0 = smem_u32(sb + st.slot * p.b_bytes);
+#pragma unroll
+                for (int kk = 0; kk < kStep / 16; ++kk) {
+                    const uint64_t ad = umma_desc_sw128(a0 + 32 * kk);
+                    const uint64_t bd = BACKWARD ? desc_mn_sw128(b0 + 2048 * kk) : umma_desc_sw128(b0 + 32 * kk);
+                    umma_bf16_pair(d, ad, bd, idesc0, i > 0 || kk > 0);
+                    if (BACKWARD && n1)      // the outputs behind this CTA's first 128: the third group of 64
+                        umma_bf16_pair(d + 256, ad, desc_mn_sw128(b0 + 16384 + 2048 * kk), idesc1, i > 0 || kk > 0);
+                }
+                umma_commit_pair(&empty[st.slot], 3);
+                st.advance(stages);
+            }
+            if (ok) umma_commit_pair(&acc_full[acc.slot], 3);
+            acc.advance(nacc);
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------------- codes to BF16
+        const int id = threadIdx.x - 256;
+        // Task q of a thread: block of 32 codes (row, blk) of the codes tile.  Neighbouring lanes take
+        // neighbouring rows, whose 16-byte chunks the swizzle spreads over the banks.
+        const int rows = BACKWARD ? kStep : half, blks = BACKWARD ? half / 32 : 2;
+        int trow[kMaxTasks], tblk[kMaxTasks];
+        uint32_t src[kMaxTasks], dst[kMaxTasks], swz[kMaxTasks];
+        bool live[kMaxTasks];
+#pragma unroll
+        for (int q = 0; q < kMaxTasks; ++q) {
+            const int task = id + q * kDeqThreads;
+            live[q] = task < rows * blks;
+            const int r = live[q] ? task % rows : 0, b = live[q] ? task / rows : 0;
+            trow[q] = r;
+            tblk[q] = b;
+            src[q] = r * p.w_pitch + ((b ^ ((r >> p.w_swz_shift) & p.w_swz_mask)) << 4);
+            // forward: 64 k of an output, block b the half b; backward: 64 outputs of a row n, group b / 2
+            dst[q] = BACKWARD ? (b >> 1) * 8192 + r * 128 : r * 128;
+            swz[q] = (((b & 1) * 4) ^ (r & 7)) << 4;
+        }
+        const uint32_t sw0 = smem_u32(sw), sb0 = smem_u32(sb);
+        pdl_wait();
+        Ring st, cs;
+        long long fill = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += pairs) {
+            const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
+            const uint8_t *sp[kMaxTasks];
+            int left[kMaxTasks];                  // stages whose block lies inside W
+#pragma unroll
+            for (int q = 0; q < kMaxTasks; ++q) {
+                if constexpr (BACKWARD) {
+                    const int blk = j0 / 32 + tblk[q];
+                    sp[q] = p.ws + static_cast<long long>(trow[q]) * p.ks + blk;
+                    left[q] = live[q] && blk < p.ks ? (p.C - trow[q] + kStep - 1) / kStep : 0;
+                } else {
+                    const int j = j0 + trow[q];
+                    sp[q] = p.ws + static_cast<long long>(j) * p.ks + tblk[q];
+                    left[q] = live[q] && j < p.J ? (p.ks - tblk[q] + 1) / 2 : 0;
+                }
+            }
+            const long long hop = BACKWARD ? static_cast<long long>(kStep) * p.ks : 2;
+            // scale bytes, four stages ahead; behind the edge 127 (codes there are filled with zeros)
+            uint32_t e[4][kMaxTasks];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int q = 0; q < kMaxTasks; ++q) e[u][q] = u < left[q] ? __ldg(sp[q] + u * hop) : 127u;
+            for (int i0 = 0; i0 < steps && ok; i0 += 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + u;
+                    if (i >= steps) break;
+                    if (!mbar_wait(&w_full[cs.slot], cs.phase)) { ok = false; break; }
+                    uint4 c[kMaxTasks];
+#pragma unroll
+                    for (int q = 0; q < kMaxTasks; ++q)
+                        if (live[q]) c[q] = lds128(sw0 + cs.slot * p.w_bytes + src[q]);
+                    if (fill >= stages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
+                    ++fill;
+                    const uint32_t to = sb0 + st.slot * p.b_bytes;
+#pragma unroll
+                    for (int q = 0; q < kMaxTasks; ++q) {
+                        if (live[q]) {
+                            const Factor f = factor_of(e[u][q]);
+                            e[u][q] = i + 4 < left[q] ? __ldg(sp[q] + static_cast<long long>(i + 4) * hop) : 127u;
+                            const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+#pragma unroll
+                            for (int jj = 0; jj < 4; ++jj) {
+                                uint32_t r[4];
+                                expand8(w[jj], f, r);
+                                sts128(to + dst[q] + (swz[q] ^ (jj << 4)), make_uint4(r[0], r[1], r[2], r[3]));
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&w_empty[cs.slot]);
+                        if (leader) mbar_arrive(&ready[st.slot]);
+                        else mbar_arrive(&expd[st.slot]);
+                    }
+                    cs.advance(kWSlots);
+                    st.advance(stages);
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------- epilogue
+        const int quarter = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        pdl_wait();
+        Ring acc;
+        for (int t = first; t < p.tiles; t += pairs) {
+            const long long m = static_cast<long long>(t % p.tiles_m) * 2 * kRows + rank * kRows + quarter * 32 + lane;
+            const int j0 = t / p.tiles_m * p.bn;
+            if (!mbar_wait(&acc_full[acc.slot], acc.phase)) break;
+            tc_fence_after();
+            for (int c = 0; c < p.bn; c += 32) {
+                __syncwarp();                   // the loads are collective
+                uint32_t r[32];
+                tmem_ld32(tmem + lanes + acc.slot * 256 + c, r);
+                tmem_ld_wait_regs(r);
+                int j = j0 + c;                 // columns in order, but for the second MMA's
+                if (BACKWARD && p.bn > 256) {
+                    const int w = half - 128, cc = c - 256;
+                    j = j0 + (c < 256 ? (c / 128) * half + c % 128 : cc / w * half + 128 + cc % w);
+                }
+                if (m < p.M && j < p.J) write_columns(p, m, j, r);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc.slot);
+            acc.advance(nacc);
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+    __syncwarp();
+    cluster_sync_all();   // no CTA leaves while its peer may still signal it
+}
+
+}  // namespace mxg
+}  // namespace w4a16

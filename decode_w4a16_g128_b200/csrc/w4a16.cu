@@ -49,6 +49,7 @@ struct DeviceInfo {
     bool gemm_ok = false;     // the GEMM's register split fits its launch allocation
     int gemm_clusters = 0;    // CTA pairs of the GEMM resident at once (its persistent grid)
     int gemm_max_splits = 4;  // K splits of the GEMM: 8 where clusters of 16 CTAs can be resident
+    bool mx_ready = false;    // the MXFP4 kernels' attributes are set
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 

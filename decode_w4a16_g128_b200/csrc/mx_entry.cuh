@@ -155,6 +155,7 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     p.stages = mxg::kMaxStages;
     while (mxg::smem_bytes(p.stages, p.b_bytes, p.w_bytes) > mxg::kSmemBudget) --p.stages;
     p.epilogue = epilogue;
+    p.scales16 = p.ks % 16 == 0 && aligned16(ws);
     const int smem = mxg::smem_bytes(p.stages, p.b_bytes, p.w_bytes);
 
     CUtensorMap tx, tw;

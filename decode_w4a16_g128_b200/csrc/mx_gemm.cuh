@@ -19,8 +19,8 @@
 //
 // Roles (512 threads): warp 0 x by TMA, warp 1 MMA issue (leader) and tensor memory, warp 2 codes by
 // TMA, warp 3 of the peer forwards "expanded" to the leader, warps 4-7 epilogue, warps 8-15 expand
-// codes.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's eight expanding warps, the
-// peer's forwarder), empty[s] (both CTAs; the stage's MMAs completed), exp[s] (peer: its eight
+// codes.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's two expanding warps, the
+// peer's forwarder), empty[s] (both CTAs; the stage's MMAs completed), exp[s] (peer: its two
 // expanding warps), w_full / w_empty (codes ring), acc_full / acc_empty (accumulators).
 #pragma once
 
@@ -40,7 +40,7 @@ constexpr int kTmemCols = 512;
 constexpr int kMaxBN = 320;              // outputs of a pair (forward: 256)
 constexpr int kBarBytes = 512;
 constexpr int kSmemBudget = 227 * 1024;
-constexpr int kMaxTasks = 2;             // blocks of 32 codes of a thread and stage
+constexpr int kTeams = 4, kTeamWarps = kDeqWarps / kTeams;   // expanding warps, see there
 
 enum Epilogue { kPlain = 0, kGated = 1, kGatedBackward = 2 };
 
@@ -57,6 +57,7 @@ struct Params {
     int w_pitch;              // bytes of a codes tile row
     int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
     int epilogue;
+    int scales16;             // rows of scale bytes start on 16-byte boundaries
 };
 
 // Dynamic shared memory: stages x (A, B), codes ring, barriers, and slack for 1024-byte alignment.
@@ -65,12 +66,6 @@ __host__ __device__ constexpr int smem_bytes(int stages, int b_bytes, int w_byte
 }
 
 // ------------------------------------------------------------------ PTX
-
-// Arrive (release, cluster scope) on an mbarrier of another CTA: what this thread has seen
-// written, through barriers too, is visible there.
-__device__ __forceinline__ void arrive_cluster_release(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
 
 // Bounded wait of the MMA issuer, acquire at cluster scope (the peer's expanded codes are behind it).
 __device__ __forceinline__ bool wait_cluster_spin(uint64_t *bar, uint32_t parity) {
@@ -229,6 +224,37 @@ struct Ring {
     }
 };
 
+// ------------------------------------------------------------------ scale bytes of a team's stages
+
+// Forward: the bytes of blocks 2i, 2i + 1 (bits 0-15) and 2i + 8, 2i + 9 (bits 16-31) of row j, i.e.
+// of stages i and i + 4; 127 outside W, where the codes are filled with zeros.  One 16-byte load
+// where rows of scale bytes are 16-byte aligned: every lane reads another row, so a load costs a
+// cache line a lane whatever its width.
+__device__ __forceinline__ uint32_t scales_by_row(const Params &p, int j, int i, bool live) {
+    if (!live || j >= p.J) return 0x7F7F7F7Fu;
+    const uint8_t *row = p.ws + static_cast<long long>(j) * p.ks;
+    const int b = 2 * i;
+    if (p.scales16) {
+        if ((b & ~15) >= p.ks) return 0x7F7F7F7Fu;
+        const uint4 v = ldg_nc_v4(row + (b & ~15));
+        const int h = i & 7;                               // 0..3: a team's first stage of the eight
+        const uint32_t lo = h < 2 ? v.x : v.y, hi = h < 2 ? v.z : v.w;
+        return h & 1 ? prmt(lo, hi, 0x7632u) : prmt(lo, hi, 0x5410u);
+    }
+    uint32_t v = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int k = b + (q & 1) + (q & 2) * 4;
+        v |= (k < p.ks ? static_cast<uint32_t>(__ldg(row + k)) : 127u) << (8 * q);
+    }
+    return v;
+}
+
+// Backward: the byte of row n, block b.
+__device__ __forceinline__ uint32_t scale_by_column(const Params &p, int n, int b, bool live) {
+    return live && n < p.C && b < p.ks ? __ldg(p.ws + static_cast<long long>(n) * p.ks + b) : 127u;
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <bool BACKWARD>
@@ -256,13 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (threadIdx.x == 0) {
         pdl_launch_dependents();
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&ready[i], 1 + kDeqWarps + 1);
+            mbar_init(&ready[i], 1 + kTeamWarps + 1);
             mbar_init(&empty[i], 1);
-            mbar_init(&expd[i], kDeqWarps);
+            mbar_init(&expd[i], kTeamWarps);
         }
         for (int i = 0; i < kWSlots; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kDeqWarps);
+            mbar_init(&w_empty[i], kTeamWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -329,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             bool ok = true;
             for (int i = 0; i < steps && ok; ++i) {
                 ok = mbar_wait(&expd[st.slot], st.phase);
-                if (ok) arrive_cluster_release(ready_l + 8 * st.slot);
+                if (ok) mbar_arrive_cluster(ready_l + 8 * st.slot);
                 st.advance(stages);
             }
             if (!ok) break;
@@ -367,89 +393,105 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- codes to BF16
-        const int id = threadIdx.x - 256;
-        // Task q of a thread: block of 32 codes (row, blk) of the codes tile.  Neighbouring lanes take
-        // neighbouring rows, whose 16-byte chunks the swizzle spreads over the banks.
+        // Four teams of two warps, each every fourth stage: expanding one stage is a chain of waits,
+        // loads, conversions, stores and a fence that takes longer than the stage's MMAs, so four
+        // stages are under way at once.
+        const int team = (warp - 8) >> 1, id = threadIdx.x & 63;
+        // Task q of a thread: block of 32 codes (row r, block b) of the codes tile.  Forward: rows of
+        // neighbouring lanes, both blocks of a row; backward: the blocks of a row side by side.
         const int rows = BACKWARD ? kStep : half, blks = BACKWARD ? half / 32 : 2;
+        const uint32_t sw0 = smem_u32(sw), sb0 = smem_u32(sb);
+        constexpr int kMaxTasks = BACKWARD ? kMaxBN / 64 : 4;
+        uint32_t src[kMaxTasks], dst[kMaxTasks];
         int trow[kMaxTasks], tblk[kMaxTasks];
-        uint32_t src[kMaxTasks], dst[kMaxTasks], swz[kMaxTasks];
-        bool live[kMaxTasks];
 #pragma unroll
         for (int q = 0; q < kMaxTasks; ++q) {
-            const int task = id + q * kDeqThreads;
-            live[q] = task < rows * blks;
-            const int r = live[q] ? task % rows : 0, b = live[q] ? task / rows : 0;
-            trow[q] = r;
-            tblk[q] = b;
-            src[q] = r * p.w_pitch + ((b ^ ((r >> p.w_swz_shift) & p.w_swz_mask)) << 4);
-            // forward: 64 k of an output, block b the half b; backward: 64 outputs of a row n, group b / 2
-            dst[q] = BACKWARD ? (b >> 1) * 8192 + r * 128 : r * 128;
-            swz[q] = (((b & 1) * 4) ^ (r & 7)) << 4;
-        }
-        const uint32_t sw0 = smem_u32(sw), sb0 = smem_u32(sb);
-        pdl_wait();
-        Ring st, cs;
-        long long fill = 0;
-        bool ok = true;
-        for (int t = first; t < p.tiles && ok; t += pairs) {
-            const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
-            const uint8_t *sp[kMaxTasks];
-            int left[kMaxTasks];                  // stages whose block lies inside W
-#pragma unroll
-            for (int q = 0; q < kMaxTasks; ++q) {
-                if constexpr (BACKWARD) {
-                    const int blk = j0 / 32 + tblk[q];
-                    sp[q] = p.ws + static_cast<long long>(trow[q]) * p.ks + blk;
-                    left[q] = live[q] && blk < p.ks ? (p.C - trow[q] + kStep - 1) / kStep : 0;
-                } else {
-                    const int j = j0 + trow[q];
-                    sp[q] = p.ws + static_cast<long long>(j) * p.ks + tblk[q];
-                    left[q] = live[q] && j < p.J ? (p.ks - tblk[q] + 1) / 2 : 0;
-                }
+            int r, b;
+            if constexpr (BACKWARD) {
+                r = (id + 64 * q) / blks;
+                b = (id + 64 * q) - r * blks;
+            } else {
+                r = id + 64 * (q >> 1);
+                b = q & 1;
             }
-            const long long hop = BACKWARD ? static_cast<long long>(kStep) * p.ks : 2;
-            // scale bytes, four stages ahead; behind the edge 127 (codes there are filled with zeros)
-            uint32_t e[4][kMaxTasks];
+            trow[q] = r < rows ? r : -1;
+            tblk[q] = b;
+            src[q] = sw0 + r * p.w_pitch + ((b ^ ((r >> p.w_swz_shift) & p.w_swz_mask)) << 4);
+            // forward: 64 k of an output, block b the half b; backward: 64 outputs of a row n, group b / 2
+            dst[q] = sb0 + (BACKWARD ? (b >> 1) * 8192 + r * 128 : r * 128) + ((((b & 1) * 4) ^ (r & 7)) << 4);
+        }
+        pdl_wait();
+        // this team's positions in the rings: stage f = team, team + 4, ...
+        int slot = team % stages, cslot = team;
+        uint32_t phase = team / stages, cphase = 0;
+        long long f = team, base = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += pairs, base += steps) {
+            const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
+            const int i0 = static_cast<int>(f - base);
+            uint32_t cur[kMaxTasks], nxt[kMaxTasks];
+            if constexpr (BACKWARD) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+                for (int q = 0; q < kMaxTasks; ++q) nxt[q] = scale_by_column(p, i0 * kStep + trow[q], j0 / 32 + tblk[q], trow[q] >= 0);
+            } else {
 #pragma unroll
-                for (int q = 0; q < kMaxTasks; ++q) e[u][q] = u < left[q] ? __ldg(sp[q] + u * hop) : 127u;
-            for (int i0 = 0; i0 < steps && ok; i0 += 4) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = i0 + u;
-                    if (i >= steps) break;
-                    if (!mbar_wait(&w_full[cs.slot], cs.phase)) { ok = false; break; }
-                    uint4 c[kMaxTasks];
-#pragma unroll
-                    for (int q = 0; q < kMaxTasks; ++q)
-                        if (live[q]) c[q] = lds128(sw0 + cs.slot * p.w_bytes + src[q]);
-                    if (fill >= stages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
-                    ++fill;
-                    const uint32_t to = sb0 + st.slot * p.b_bytes;
+                for (int q = 0; q < kMaxTasks; q += 2) nxt[q] = scales_by_row(p, j0 + trow[q], i0, trow[q] >= 0);
+            }
+            for (int i = i0, it = 0; i < steps; i += 4, ++it, f += 4) {
+                if constexpr (BACKWARD) {
 #pragma unroll
                     for (int q = 0; q < kMaxTasks; ++q) {
-                        if (live[q]) {
-                            const Factor f = factor_of(e[u][q]);
-                            e[u][q] = i + 4 < left[q] ? __ldg(sp[q] + static_cast<long long>(i + 4) * hop) : 127u;
-                            const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+                        cur[q] = nxt[q];
+                        nxt[q] = scale_by_column(p, (i + 4) * kStep + trow[q], j0 / 32 + tblk[q], trow[q] >= 0);
+                    }
+                } else {
+                    // four scale bytes of a row: this stage's two and the next one's of this team
 #pragma unroll
-                            for (int jj = 0; jj < 4; ++jj) {
-                                uint32_t r[4];
-                                expand8(w[jj], f, r);
-                                sts128(to + dst[q] + (swz[q] ^ (jj << 4)), make_uint4(r[0], r[1], r[2], r[3]));
-                            }
+                    for (int q = 0; q < kMaxTasks; q += 2) {
+                        if (it & 1) {
+                            cur[q] >>= 16;
+                        } else {
+                            cur[q] = nxt[q];
+                            nxt[q] = scales_by_row(p, j0 + trow[q], i + 8, trow[q] >= 0);
                         }
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&w_empty[cs.slot]);
-                        if (leader) mbar_arrive(&ready[st.slot]);
-                        else mbar_arrive(&expd[st.slot]);
+                }
+                if (!mbar_wait(&w_full[cslot], cphase)) { ok = false; break; }
+                uint4 c[kMaxTasks];
+#pragma unroll
+                for (int q = 0; q < kMaxTasks; ++q)
+                    if (trow[q] >= 0) c[q] = lds128(src[q] + cslot * p.w_bytes);
+                if (f >= stages && !mbar_wait(&empty[slot], phase ^ 1u)) { ok = false; break; }
+                const uint32_t to = slot * p.b_bytes;
+#pragma unroll
+                for (int q = 0; q < kMaxTasks; ++q) {
+                    if (trow[q] >= 0) {
+                        const Factor fac = factor_of(BACKWARD ? cur[q] : (cur[q & ~1] >> (8 * (q & 1))) & 255u);
+                        const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj) {
+                            uint32_t r[4];
+                            expand8(w[jj], fac, r);
+                            sts128((to + dst[q]) ^ (jj << 4), make_uint4(r[0], r[1], r[2], r[3]));
+                        }
                     }
-                    cs.advance(kWSlots);
-                    st.advance(stages);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&w_empty[cslot]);
+                    if (leader) mbar_arrive(&ready[slot]);
+                    else mbar_arrive(&expd[slot]);
+                }
+                slot += 4;
+                if (slot >= stages) {
+                    slot -= stages;
+                    phase ^= 1u;
+                }
+                cslot += 4;
+                if (cslot >= kWSlots) {
+                    cslot -= kWSlots;
+                    cphase ^= 1u;
                 }
             }
         }

@@ -137,10 +137,11 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     p.tiles = static_cast<int>(tiles);
     const int half = p.bn / 2;
     p.b_bytes = backward ? (half + 63) / 64 * 8192 : half * 128;
-    p.w_bytes = 32 * half;
-    p.w_pitch = backward ? half / 2 : 32;
-    // codes tile: rows of 32 and 64 bytes are swizzled by the copy (else neighbouring rows' 16-byte
-    // chunks would share banks); 16-byte chunks at a pitch of 48 or 80 bytes spread by themselves
+    p.w_bytes = backward ? 32 * half : 128 * half;
+    p.w_slots = backward ? 8 : 3;
+    p.w_pitch = backward ? half / 2 : 128;
+    // codes tile: rows of 32, 64 and 128 bytes are swizzled by the copy (else neighbouring rows'
+    // 16-byte chunks would share banks); chunks at a pitch of 48 or 80 bytes spread by themselves
     CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE;
     p.w_swz_shift = p.w_swz_mask = 0;
     if (p.w_pitch == 32) {
@@ -151,19 +152,20 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
         swz = CU_TENSOR_MAP_SWIZZLE_64B;
         p.w_swz_shift = 1;
         p.w_swz_mask = 3;
+    } else if (p.w_pitch == 128) {
+        swz = CU_TENSOR_MAP_SWIZZLE_128B;
     }
     p.stages = mxg::kMaxStages;
-    while (mxg::smem_bytes(p.stages, p.b_bytes, p.w_bytes) > mxg::kSmemBudget) --p.stages;
+    while (mxg::smem_bytes(p.stages, p.b_bytes, p.w_slots, p.w_bytes) > mxg::kSmemBudget) --p.stages;
     p.epilogue = epilogue;
     p.scales16 = p.ks % 16 == 0 && aligned16(ws);
-    const int smem = mxg::smem_bytes(p.stages, p.b_bytes, p.w_bytes);
+    const int smem = mxg::smem_bytes(p.stages, p.b_bytes, p.w_slots, p.w_bytes);
 
     CUtensorMap tx, tw;
     int rc = encode_2d(d, &tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a, C, M, C * 2, mxg::kStep, mxg::kRows,
                        CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
-    rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : mxg::kStep / 8,
-                   backward ? mxg::kStep : half, swz);
+    rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : 32, backward ? mxg::kStep : half, swz);
     if (rc) return rc;
     const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)), 1, 1);
     const auto kernel = backward ? mxg::gemm_kernel<true> : mxg::gemm_kernel<false>;

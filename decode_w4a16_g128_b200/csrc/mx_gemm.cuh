@@ -34,7 +34,12 @@ constexpr int kRows = 128;               // x rows of a CTA
 constexpr int kStep = 64;                // contraction of a stage
 constexpr int kABytes = kRows * kStep * 2;
 constexpr int kMaxStages = 8;
-constexpr int kWSlots = 8;
+constexpr int kMaxWSlots = 8;
+// Stages of a codes copy.  A copy costs the TMA unit time per row, whatever the row's length (a copy
+// of 128 rows x 32 bytes a stage, beside x's 128 rows, held the whole pipeline to about 800 cycles
+// a stage): forward rows are fetched 128 bytes at a time, K = 256, for the four teams' stages.
+template <bool BACKWARD>
+constexpr int kWSpan = BACKWARD ? 1 : 4;
 constexpr int kDeqWarps = 8, kDeqThreads = 32 * kDeqWarps, kEpiWarps = 4;
 constexpr int kTmemCols = 512;
 constexpr int kMaxBN = 320;              // outputs of a pair (forward: 256)
@@ -53,7 +58,8 @@ struct Params {
     int bn;                   // outputs of a pair
     int tiles_m, tiles;
     int stages;
-    int b_bytes, w_bytes;     // B tile and codes tile of a CTA and stage
+    int b_bytes, w_bytes;     // B tile of a CTA and stage, codes of a copy
+    int w_slots;              // codes ring
     int w_pitch;              // bytes of a codes tile row
     int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
     int epilogue;
@@ -61,37 +67,21 @@ struct Params {
 };
 
 // Dynamic shared memory: stages x (A, B), codes ring, barriers, and slack for 1024-byte alignment.
-__host__ __device__ constexpr int smem_bytes(int stages, int b_bytes, int w_bytes) {
-    return stages * (kABytes + b_bytes) + kWSlots * w_bytes + kBarBytes + 1024;
+__host__ __device__ constexpr int smem_bytes(int stages, int b_bytes, int w_slots, int w_bytes) {
+    return stages * (kABytes + b_bytes) + w_slots * w_bytes + kBarBytes + 1024;
 }
 
 // ------------------------------------------------------------------ PTX
 
-// Bounded wait of the MMA issuer, acquire at cluster scope (the peer's expanded codes are behind it).
-__device__ __forceinline__ bool wait_cluster_spin(uint64_t *bar, uint32_t parity) {
-    auto test = [&]() {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        return ok != 0;
-    };
-    if (test()) return true;
-    const unsigned long long t0 = globaltimer();
-    for (uint32_t spin = 1;; ++spin) {
-        if (test()) return true;
-        if ((spin & 1023u) == 0) {
-            if (status_set()) return false;
-            if (globaltimer() - t0 > kWaitTimeoutNs) {
-                record_timeout();
-                return false;
-            }
-        }
-    }
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 // D[tmem] (+)= A[smem] . B[smem] of a CTA pair, issued by the leader.
@@ -226,28 +216,34 @@ struct Ring {
 
 // ------------------------------------------------------------------ scale bytes of a team's stages
 
-// Forward: the bytes of blocks 2i, 2i + 1 (bits 0-15) and 2i + 8, 2i + 9 (bits 16-31) of row j, i.e.
-// of stages i and i + 4; 127 outside W, where the codes are filled with zeros.  One 16-byte load
-// where rows of scale bytes are 16-byte aligned: every lane reads another row, so a load costs a
-// cache line a lane whatever its width.
-__device__ __forceinline__ uint32_t scales_by_row(const Params &p, int j, int i, bool live) {
-    if (!live || j >= p.J) return 0x7F7F7F7Fu;
+// Forward, stage i of team i % 4 with i % 8 < 4: what scale_bytes needs of row j for stages i and i + 4;
+// 127 outside W, where the codes are filled with zeros.  One 16-byte load where rows of scale bytes
+// are 16-byte aligned (every lane reads another row, so a load costs a cache line a lane whatever its
+// width), else four bytes.  The words are kept as loaded and looked at two stages later: a look here
+// would wait for the load.
+__device__ __forceinline__ uint4 scale_words(const Params &p, int j, int i, bool live) {
+    uint4 v = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if (!live || j >= p.J) return v;
     const uint8_t *row = p.ws + static_cast<long long>(j) * p.ks;
     const int b = 2 * i;
     if (p.scales16) {
-        if ((b & ~15) >= p.ks) return 0x7F7F7F7Fu;
-        const uint4 v = ldg_nc_v4(row + (b & ~15));
-        const int h = i & 7;                               // 0..3: a team's first stage of the eight
-        const uint32_t lo = h < 2 ? v.x : v.y, hi = h < 2 ? v.z : v.w;
-        return h & 1 ? prmt(lo, hi, 0x7632u) : prmt(lo, hi, 0x5410u);
-    }
-    uint32_t v = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int k = b + (q & 1) + (q & 2) * 4;
-        v |= (k < p.ks ? static_cast<uint32_t>(__ldg(row + k)) : 127u) << (8 * q);
+        if ((b & ~15) < p.ks) v = ldg_nc_v4(row + (b & ~15));
+    } else {
+        if (b < p.ks) v.x = __ldg(row + b);
+        if (b + 1 < p.ks) v.y = __ldg(row + b + 1);
+        if (b + 8 < p.ks) v.z = __ldg(row + b + 8);
+        if (b + 9 < p.ks) v.w = __ldg(row + b + 9);
     }
     return v;
+}
+
+// The bytes of blocks 2i, 2i + 1 (stage i, bits 0-15) and 2i + 8, 2i + 9 (stage i + 4, bits 16-31).
+__device__ __forceinline__ uint32_t scale_bytes(const Params &p, const uint4 &v, int team) {
+    if (p.scales16) {
+        const uint32_t lo = team < 2 ? v.x : v.y, hi = team < 2 ? v.z : v.w;
+        return team & 1 ? prmt(lo, hi, 0x7632u) : prmt(lo, hi, 0x5410u);
+    }
+    return prmt(prmt(v.x, v.y, 0x0040u), prmt(v.z, v.w, 0x0040u), 0x5410u);
 }
 
 // Backward: the byte of row n, block b.
@@ -264,12 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int stages = p.stages;
     uint8_t *sa = smem, *sb = sa + stages * kABytes, *sw = sb + stages * p.b_bytes;
-    uint64_t *ready = reinterpret_cast<uint64_t *>(sw + kWSlots * p.w_bytes);
+    uint64_t *ready = reinterpret_cast<uint64_t *>(sw + p.w_slots * p.w_bytes);
     uint64_t *empty = ready + kMaxStages, *expd = empty + kMaxStages;
-    uint64_t *w_full = expd + kMaxStages, *w_empty = w_full + kWSlots;
-    uint64_t *acc_full = w_empty + kWSlots, *acc_empty = acc_full + 2;
+    uint64_t *w_full = expd + kMaxStages, *w_empty = w_full + kMaxWSlots;
+    uint64_t *acc_full = w_empty + kMaxWSlots, *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
-    static_assert((3 * kMaxStages + 2 * kWSlots + 4) * 8 + 8 <= kBarBytes, "barrier area");
+    static_assert((3 * kMaxStages + 2 * kMaxWSlots + 4) * 8 + 8 <= kBarBytes, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -286,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&empty[i], 1);
             mbar_init(&expd[i], kTeamWarps);
         }
-        for (int i = 0; i < kWSlots; ++i) {
+        for (int i = 0; i < kMaxWSlots; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kTeamWarps);
+            mbar_init(&w_empty[i], kWSpan<BACKWARD> * kTeamWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -330,24 +326,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // ---------------------------------------------------------------- codes by TMA
         prefetch_tmap(&tm_w);
         pdl_wait();
+        const int slots = p.w_slots;
         Ring st;
         long long issued = 0;
         bool ok = true;
         for (int t = first; t < p.tiles && ok; t += pairs) {
             const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
-            for (int i = 0; i < steps; ++i) {
-                if (issued >= kWSlots && !mbar_wait(&w_empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
+            for (int i = 0; i < steps; i += kWSpan<BACKWARD>) {
+                if (issued >= slots && !mbar_wait(&w_empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
                 mbar_arrive_expect_tx(&w_full[st.slot], p.w_bytes);
                 if constexpr (BACKWARD)
                     tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], j0 / 8, i * kStep);
                 else
                     tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], i * (kStep / 8), j0);
                 ++issued;
-                st.advance(kWSlots);
+                st.advance(slots);
             }
         }
-        for (long long j = issued > kWSlots ? issued - kWSlots : 0; j < issued; ++j)
-            mbar_wait(&w_full[j % kWSlots], static_cast<uint32_t>((j / kWSlots) & 1), false);
+        for (long long j = issued > slots ? issued - slots : 0; j < issued; ++j)
+            mbar_wait(&w_full[j % slots], static_cast<uint32_t>((j / slots) & 1), false);
     } else if (warp == 3 && lane == 0 && !leader) {
         // ---------------------------------------------------------------- "expanded", to the leader
         Ring st;
@@ -360,8 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (!ok) break;
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ---------------------------------------------------------------- MMA issue
+        // The warp stays converged and one elected lane issues: with the loop in one lane's branch
+        // the same instructions took 10 to 15 % longer (the descriptors are uniform registers, which
+        // divergent code has to move there one lane at a time).
         const int n0 = p.bn < 256 ? p.bn : 256, n1 = p.bn - n0;
         const uint32_t major = BACKWARD ? kIdescBMnMajor : 0u;
         const uint32_t idesc0 = umma_idesc_bf16(2 * kRows, n0) | major, idesc1 = umma_idesc_bf16(2 * kRows, n1) | major;
@@ -374,21 +374,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             tc_fence_after();
             const uint32_t d = tmem + acc.slot * 256;
             for (int i = 0; i < steps; ++i) {
-                if (!wait_cluster_spin(&ready[st.slot], st.phase)) { ok = false; break; }
-                tc_fence_after();
+                if (!mbar_wait_spin(&ready[st.slot], st.phase)) ok = false;
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 const uint32_t a0 = smem_u32(sa + st.slot * kABytes), b0 = smem_u32(sb + st.slot * p.b_bytes);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kStep / 16; ++kk) {
-                    const uint64_t ad = umma_desc_sw128(a0 + 32 * kk);
-                    const uint64_t bd = BACKWARD ? desc_mn_sw128(b0 + 2048 * kk) : umma_desc_sw128(b0 + 32 * kk);
-                    umma_bf16_pair(d, ad, bd, idesc0, i > 0 || kk > 0);
-                    if (BACKWARD && n1)      // the outputs behind this CTA's first 128: the third group of 64
-                        umma_bf16_pair(d + 256, ad, desc_mn_sw128(b0 + 16384 + 2048 * kk), idesc1, i > 0 || kk > 0);
+                    for (int kk = 0; kk < kStep / 16; ++kk) {
+                        const uint64_t ad = umma_desc_sw128(a0 + 32 * kk);
+                        const uint64_t bd = BACKWARD ? desc_mn_sw128(b0 + 2048 * kk) : umma_desc_sw128(b0 + 32 * kk);
+                        umma_bf16_pair(d, ad, bd, idesc0, i > 0 || kk > 0);
+                        if (BACKWARD && n1)      // the outputs behind this CTA's first 128: the third group of 64
+                            umma_bf16_pair(d + 256, ad, desc_mn_sw128(b0 + 16384 + 2048 * kk), idesc1, i > 0 || kk > 0);
+                    }
+                    umma_commit_pair(&empty[st.slot], 3);
                 }
-                umma_commit_pair(&empty[st.slot], 3);
                 st.advance(stages);
             }
-            if (ok) umma_commit_pair(&acc_full[acc.slot], 3);
+            if (ok && elect_one()) umma_commit_pair(&acc_full[acc.slot], 3);
             acc.advance(nacc);
         }
     } else if (warp >= 8) {
@@ -416,26 +418,35 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             trow[q] = r < rows ? r : -1;
             tblk[q] = b;
-            src[q] = sw0 + r * p.w_pitch + ((b ^ ((r >> p.w_swz_shift) & p.w_swz_mask)) << 4);
+            // forward: chunk 2 (i % 4) + b of a 128-byte row, i % 4 the team
+            src[q] = sw0 + (BACKWARD ? r * p.w_pitch + ((b ^ ((r >> p.w_swz_shift) & p.w_swz_mask)) << 4)
+                                     : r * 128 + (((2 * team + b) ^ (r & 7)) << 4));
             // forward: 64 k of an output, block b the half b; backward: 64 outputs of a row n, group b / 2
             dst[q] = sb0 + (BACKWARD ? (b >> 1) * 8192 + r * 128 : r * 128) + ((((b & 1) * 4) ^ (r & 7)) << 4);
         }
         pdl_wait();
-        // this team's positions in the rings: stage f = team, team + 4, ...
-        int slot = team % stages, cslot = team;
-        uint32_t phase = team / stages, cphase = 0;
-        long long f = team, base = 0;
+        constexpr int kSpan = kWSpan<BACKWARD>;
+        const int slots = p.w_slots;
+        const int copies = (steps + kSpan - 1) / kSpan;        // of a tile
+        long long base = 0, wbase = 0;                         // stages and copies of the tiles before
         bool ok = true;
-        for (int t = first; t < p.tiles && ok; t += pairs, base += steps) {
+        for (int t = first; t < p.tiles && ok; t += pairs, base += steps, wbase += copies) {
             const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
-            const int i0 = static_cast<int>(f - base);
-            uint32_t cur[kMaxTasks], nxt[kMaxTasks];
+            const int i0 = team;                               // this team's stages: team, team + 4, ...
+            long long f = base + i0;
+            int slot = static_cast<int>(f % stages);
+            uint32_t phase = static_cast<uint32_t>(f / stages) & 1u;
+            const long long wf = wbase + i0 / kSpan;
+            int cslot = static_cast<int>(wf % slots);
+            uint32_t cphase = static_cast<uint32_t>(wf / slots) & 1u;
+            uint32_t cur[kMaxTasks], nxt[BACKWARD ? kMaxTasks : 1];
+            uint4 words[BACKWARD ? 1 : kMaxTasks / 2];
             if constexpr (BACKWARD) {
 #pragma unroll
                 for (int q = 0; q < kMaxTasks; ++q) nxt[q] = scale_by_column(p, i0 * kStep + trow[q], j0 / 32 + tblk[q], trow[q] >= 0);
             } else {
 #pragma unroll
-                for (int q = 0; q < kMaxTasks; q += 2) nxt[q] = scales_by_row(p, j0 + trow[q], i0, trow[q] >= 0);
+                for (int q = 0; q < kMaxTasks; q += 2) words[q / 2] = scale_words(p, j0 + trow[q], i0, trow[q] >= 0);
             }
             for (int i = i0, it = 0; i < steps; i += 4, ++it, f += 4) {
                 if constexpr (BACKWARD) {
@@ -451,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         if (it & 1) {
                             cur[q] >>= 16;
                         } else {
-                            cur[q] = nxt[q];
-                            nxt[q] = scales_by_row(p, j0 + trow[q], i + 8, trow[q] >= 0);
+                            cur[q] = scale_bytes(p, words[q / 2], team);
+                            words[q / 2] = scale_words(p, j0 + trow[q], i + 8, trow[q] >= 0);
                         }
                     }
                 }
@@ -488,11 +499,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     slot -= stages;
                     phase ^= 1u;
                 }
-                cslot += 4;
-                if (cslot >= kWSlots) {
-                    cslot -= kWSlots;
+                cslot += 4 / kSpan;
+                if (cslot >= slots) {
+                    cslot -= slots;
                     cphase ^= 1u;
                 }
+            }
+            // a tile's last copy holds codes of up to four stages: the teams without one release it too
+            if (kSpan > 1 && ok && steps % kSpan != 0 && team >= steps % kSpan) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[cslot]);
             }
         }
     } else if (warp >= 4) {

@@ -4,8 +4,8 @@
 #pragma once
 
 #include "mx.cuh"
+#include "mx_a4.cuh"
 #include "mx_gemm.cuh"
-#include "mx_simple.cuh"
 
 namespace w4a16 {
 namespace {
@@ -45,6 +45,8 @@ int mx_device(DeviceInfo **d) {
     cudaError_t e = cudaFuncSetAttribute(mxg::gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mxg::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(mx4::a4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mx4::kSmemBytes);
     if (e != cudaSuccess) return cuda_fail(e);
     (*d)->mx_ready = true;
     return W4A16_OK;
@@ -73,31 +75,16 @@ int mx_launch(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, void 
     return e == cudaSuccess ? W4A16_OK : cuda_fail(e);
 }
 
-int mx_simple(const mxs::Params &p, bool a4, bool backward, void *stream) {
-    const int64_t gx = (p.J + mxs::kTile - 1) / mxs::kTile, gy = (p.M + mxs::kTile - 1) / mxs::kTile;
-    if (gy > 65535) return W4A16_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1);
-    if (a4) return mx_launch(mxs::product_kernel<true, false>, grid, mxs::kThreads, 0, stream, p);
-    if (backward) return mx_launch(mxs::product_kernel<false, true>, grid, mxs::kThreads, 0, stream, p);
-    return mx_launch(mxs::product_kernel<false, false>, grid, mxs::kThreads, 0, stream, p);
-}
-
-mxs::Params mx_params(const void *a, const uint32_t *aq, const uint8_t *as, const uint32_t *wq, const uint8_t *ws,
-                      const void *dh, void *out, int64_t M, int64_t J, int64_t C, int64_t K, int epilogue) {
-    mxs::Params p;
-    p.a = static_cast<const uint16_t *>(a);
-    p.aq = aq;
-    p.as = as;
-    p.wq = wq;
-    p.ws = ws;
-    p.dh = static_cast<const uint16_t *>(dh);
-    p.out = static_cast<uint16_t *>(out);
-    p.M = static_cast<int>(M);
-    p.J = static_cast<int>(J);
-    p.C = static_cast<int>(C);
-    p.K = static_cast<int>(K);
-    p.epilogue = epilogue;
-    return p;
+mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilogue) {
+    mxg::Output o;
+    o.out = static_cast<uint16_t *>(out);
+    o.dh = static_cast<const uint16_t *>(dh);
+    o.M = static_cast<int>(M);
+    o.J = static_cast<int>(J);
+    o.epilogue = epilogue;
+    const int64_t row = epilogue == mxg::kGated ? J / 2 : J;
+    o.wide = row % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+    return o;
 }
 
 // Outputs of a CTA pair: the width with the least estimated time, rounds of the persistent grid times
@@ -123,11 +110,8 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
             int64_t J, int64_t C, int64_t N, int64_t K, bool backward, int epilogue, void *stream) {
     const int pairs = d->sms / 2;
     mxg::Params p;
+    p.o = mx_output(out, dh, M, J, epilogue);
     p.ws = ws;
-    p.dh = static_cast<const uint16_t *>(dh);
-    p.out = static_cast<uint16_t *>(out);
-    p.M = static_cast<int>(M);
-    p.J = static_cast<int>(J);
     p.C = static_cast<int>(C);
     p.ks = static_cast<int>(K / mx::kBlock);
     p.bn = mx_gemm_width(M, J, backward, pairs);
@@ -157,7 +141,6 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     }
     p.stages = mxg::kMaxStages;
     while (mxg::smem_bytes(p.stages, p.b_bytes, p.w_slots, p.w_bytes) > mxg::kSmemBudget) --p.stages;
-    p.epilogue = epilogue;
     p.scales16 = p.ks % 16 == 0 && aligned16(ws);
     const int smem = mxg::smem_bytes(p.stages, p.b_bytes, p.w_slots, p.w_bytes);
 
@@ -170,6 +153,47 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)), 1, 1);
     const auto kernel = backward ? mxg::gemm_kernel<true> : mxg::gemm_kernel<false>;
     return mx_launch(kernel, grid, mxg::kThreads, smem, stream, tx, tw, p);
+}
+
+// Outputs of a CTA pair of the 4-bit product: the fewest column-rounds of the persistent grid; an MMA
+// of 64 columns takes about as long as one of 100.
+int mx_a4_width(int64_t M, int64_t N, int pairs) {
+    const int64_t tm = (M + 2 * mx4::kRows - 1) / (2 * mx4::kRows);
+    int best = 0;
+    int64_t cost = 0;
+    for (int bn = 64; bn <= mx4::kMaxBN; bn += 64) {
+        const int64_t tiles = tm * ((N + bn - 1) / bn), rounds = (tiles + pairs - 1) / pairs;
+        const int64_t c = rounds * std::max(bn, 100);
+        if (!best || c < cost) {
+            best = bn;
+            cost = c;
+        }
+    }
+    return best;
+}
+
+int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *wq, const uint8_t *ws, void *y, int64_t M,
+          int64_t N, int64_t K, void *stream) {
+    const int pairs = d->sms / 2;
+    mx4::Params p;
+    p.o = mx_output(y, nullptr, M, N, mxg::kPlain);
+    p.xs = xs;
+    p.ws = ws;
+    p.K = static_cast<int>(K);
+    p.bn = mx_a4_width(M, N, pairs);
+    const int64_t tm = (M + 2 * mx4::kRows - 1) / (2 * mx4::kRows), tiles = tm * ((N + p.bn - 1) / p.bn);
+    if (tiles >= kSizeLimit) return W4A16_ERR_UNSUPPORTED;
+    p.tiles_m = static_cast<int>(tm);
+    p.tiles = static_cast<int>(tiles);
+    CUtensorMap tx, tw;
+    int rc = encode_2d(d, &tx, CU_TENSOR_MAP_DATA_TYPE_UINT32, xq, K / 8, M, K / 2, mx4::kStep / 8, mx4::kRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+    rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, mx4::kStep / 8, p.bn / 2,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+    const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)), 1, 1);
+    return mx_launch(mx4::a4_kernel, grid, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, p);
 }
 
 unsigned stream_grid(int64_t words, int sms) {
@@ -251,7 +275,7 @@ int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(y, s[0].bytes, stream);
-    return mx_simple(mx_params(nullptr, xq, xscales, wq, scales, nullptr, y, M, N, K, K, mxs::kPlain), true, false, stream);
+    return mx_a4(d, xq, xscales, wq, scales, y, M, N, K, stream);
 }
 
 int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, void *h, int64_t M, int64_t N2, int64_t K,

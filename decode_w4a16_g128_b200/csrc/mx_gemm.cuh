@@ -47,25 +47,6 @@ constexpr int kBarBytes = 512;
 constexpr int kSmemBudget = 227 * 1024;
 constexpr int kTeams = 4, kTeamWarps = kDeqWarps / kTeams;   // expanding warps, see there
 
-enum Epilogue { kPlain = 0, kGated = 1, kGatedBackward = 2 };
-
-struct Params {
-    const uint8_t *ws;        // scales [N, K/32]
-    const uint16_t *dh;       // bf16 [M, J/2] (kGatedBackward)
-    uint16_t *out;            // bf16 [M, J], or [M, J/2] (kGated)
-    int M, J, C;              // rows, outputs, contraction
-    int ks;                   // scale bytes of a row of W (K / 32)
-    int bn;                   // outputs of a pair
-    int tiles_m, tiles;
-    int stages;
-    int b_bytes, w_bytes;     // B tile of a CTA and stage, codes of a copy
-    int w_slots;              // codes ring
-    int w_pitch;              // bytes of a codes tile row
-    int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
-    int epilogue;
-    int scales16;             // rows of scale bytes start on 16-byte boundaries
-};
-
 // Dynamic shared memory: stages x (A, B), codes ring, barriers, and slack for 1024-byte alignment.
 __host__ __device__ constexpr int smem_bytes(int stages, int b_bytes, int w_slots, int w_bytes) {
     return stages * (kABytes + b_bytes) + w_slots * w_bytes + kBarBytes + 1024;
@@ -151,26 +132,47 @@ __device__ __forceinline__ void expand8(uint32_t v, const Factor &s, uint32_t (&
 
 // ------------------------------------------------------------------ epilogue helpers
 
-__device__ __forceinline__ void store16(uint16_t *dst, const float *v) {
-    uint4 o;
-    o.x = pack_bf16x2(v[0], v[1]);
-    o.y = pack_bf16x2(v[2], v[3]);
-    o.z = pack_bf16x2(v[4], v[5]);
-    o.w = pack_bf16x2(v[6], v[7]);
-    *reinterpret_cast<uint4 *>(dst) = o;
+// Eight or sixteen values to BF16 at 16- or 32-byte boundaries.
+__device__ __forceinline__ uint4 pack8(const float *v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store32(uint16_t *dst, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+__device__ __forceinline__ void store_pair(uint16_t *dst, uint4 a, uint4 b, bool wide) {
+    if (wide) {
+        store32(dst, a, b);
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = a;
+        reinterpret_cast<uint4 *>(dst)[1] = b;
+    }
 }
 
-// 32 accumulator columns of one row: outputs j .. j + 31.
-__device__ __forceinline__ void write_columns(const Params &p, long long m, int j, const uint32_t (&r)[32]) {
+// Where a product's sums go: BF16 of them [M, J], silu(gate) up [M, J/2], or both gradients [M, J].
+enum Epilogue { kPlain = 0, kGated = 1, kGatedBackward = 2 };
+struct Output {
+    uint16_t *out;
+    const uint16_t *dh;       // bf16 [M, J/2] (kGatedBackward)
+    int M, J;
+    int epilogue;
+    int wide;                 // 32-byte stores: rows and base are multiples of 32 bytes
+};
+
+// 32 accumulator columns of one row: outputs j .. j + 31 (j a multiple of 32 or, at the start of a
+// second MMA's columns, still of 32).
+__device__ __forceinline__ void write_columns(const Output &p, long long m, int j, const uint32_t (&r)[32]) {
     if (p.epilogue == kPlain) {
         uint16_t *dst = p.out + m * p.J + j;
         if ((p.J & 7) == 0) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[8];
+            for (int q = 0; q < 2; ++q) {
+                float v[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * q + i]);
-                if (j + 8 * q < p.J) store16(dst + 8 * q, v);
+                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * q + i]);
+                if (j + 16 * q + 8 < p.J) store_pair(dst + 16 * q, pack8(v), pack8(v + 8), p.wide);
+                else if (j + 16 * q < p.J) *reinterpret_cast<uint4 *>(dst + 16 * q) = pack8(v);
             }
         } else {
 #pragma unroll
@@ -179,29 +181,50 @@ __device__ __forceinline__ void write_columns(const Params &p, long long m, int 
         }
         return;
     }
+    // J is a multiple of 16: 8 gate columns and their 8 up columns
+    const long long h = m * (p.J / 2) + j / 2;
+    if (p.epilogue == kGated) {
+        uint4 o[2];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {                 // 8 gate columns and their 8 up columns
-        if (j + 16 * q >= p.J) break;             // J is a multiple of 16
-        const long long h = m * (p.J / 2) + j / 2 + 8 * q;
-        float a[8], b[8];
-        if (p.epilogue == kGated) {
+        for (int q = 0; q < 2; ++q) {
+            float a[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 a[i] = mx::gated(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]));
-            store16(p.out + h, a);
-        } else {
-            const uint4 d = ldg_v4(p.dh + h);
-            const float dh[8] = {bf16_lo_to_f32(d.x), bf16_hi_to_f32(d.x), bf16_lo_to_f32(d.y), bf16_hi_to_f32(d.y),
-                                 bf16_lo_to_f32(d.z), bf16_hi_to_f32(d.z), bf16_lo_to_f32(d.w), bf16_hi_to_f32(d.w)};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                mx::gated_backward(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]), dh[i], a[i], b[i]);
-            uint16_t *dst = p.out + m * p.J + j + 16 * q;
-            store16(dst, a);
-            store16(dst + 8, b);
+            o[q] = pack8(a);
         }
+        if (j + 16 < p.J) store_pair(p.out + h, o[0], o[1], p.wide);
+        else *reinterpret_cast<uint4 *>(p.out + h) = o[0];
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        if (j + 16 * q >= p.J) break;
+        const uint4 d = ldg_v4(p.dh + h + 8 * q);
+        const float dh[8] = {bf16_lo_to_f32(d.x), bf16_hi_to_f32(d.x), bf16_lo_to_f32(d.y), bf16_hi_to_f32(d.y),
+                             bf16_lo_to_f32(d.z), bf16_hi_to_f32(d.z), bf16_lo_to_f32(d.w), bf16_hi_to_f32(d.w)};
+        float a[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            mx::gated_backward(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]), dh[i], a[i], b[i]);
+        store_pair(p.out + m * p.J + j + 16 * q, pack8(a), pack8(b), p.wide);
     }
 }
+
+struct Params {
+    Output o;                 // M rows, J outputs
+    const uint8_t *ws;        // scales [N, K/32]
+    int C;                    // contraction
+    int ks;                   // scale bytes of a row of W (K / 32)
+    int bn;                   // outputs of a pair
+    int tiles_m, tiles;
+    int stages;
+    int b_bytes, w_bytes;     // B tile of a CTA and stage, codes of a copy
+    int w_slots;              // codes ring
+    int w_pitch;              // bytes of a codes tile row
+    int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
+    int scales16;             // rows of scale bytes start on 16-byte boundaries
+};
 
 struct Ring {
     int slot = 0;
@@ -223,7 +246,7 @@ struct Ring {
 // would wait for the load.
 __device__ __forceinline__ uint4 scale_words(const Params &p, int j, int i, bool live) {
     uint4 v = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if (!live || j >= p.J) return v;
+    if (!live || j >= p.o.J) return v;
     const uint8_t *row = p.ws + static_cast<long long>(j) * p.ks;
     const int b = 2 * i;
     if (p.scales16) {
@@ -532,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const int w = half - 128, cc = c - 256;
                     j = j0 + (c < 256 ? (c / 128) * half + c % 128 : cc / w * half + 128 + cc % w);
                 }
-                if (m < p.M && j < p.J) write_columns(p, m, j, r);
+                if (m < p.o.M && j < p.o.J) write_columns(p.o, m, j, r);
             }
             tc_fence_before();
             __syncwarp();

@@ -6,6 +6,7 @@
 #include "mx.cuh"
 #include "mx_a4.cuh"
 #include "mx_gemm.cuh"
+#include "mx_matvec.cuh"
 
 namespace w4a16 {
 namespace {
@@ -196,6 +197,32 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
     return mx_launch(mx4::a4_kernel, grid, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, p);
 }
 
+// Few rows of x: forward products alone.
+bool mx_few_rows(int64_t M) { return M <= mxv::kMaxM; }
+
+template <int RB, int NB, int WARPS, int D>
+int mx_matvec_launch(const mxv::Params &p, void *stream) {
+    const dim3 grid(static_cast<unsigned>((int64_t(p.N) + 16 * RB - 1) / (16 * RB)), 1, 1);
+    return mx_launch(mxv::matvec_kernel<RB, NB, WARPS, D>, grid, 32 * WARPS, 0, stream, p);
+}
+
+int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *ws, void *out, int64_t M, int64_t N,
+              int64_t K, bool gated, void *stream) {
+    mxv::Params p;
+    p.x = static_cast<const uint16_t *>(x);
+    p.wq = wq;
+    p.ws = ws;
+    p.out = static_cast<uint16_t *>(out);
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.gated = gated ? 1 : 0;
+    (void)d;
+    if (M <= 8) return mx_matvec_launch<1, 1, 8, 3>(p, stream);
+    if (M <= 16) return mx_matvec_launch<1, 2, 8, 3>(p, stream);
+    return mx_matvec_launch<1, 4, 8, 2>(p, stream);
+}
+
 unsigned stream_grid(int64_t words, int sms) {
     const int64_t per = int64_t(mx::kQThreads) * mx::kQUnroll;
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((words + per - 1) / per, int64_t(sms) * 8)));
@@ -259,6 +286,7 @@ int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, vo
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(y, s[0].bytes, stream);   // an empty sum
+    if (mx_few_rows(M)) return mx_matvec(d, x, wq, scales, y, M, N, K, false, stream);
     return mx_gemm(d, x, wq, scales, nullptr, y, M, N, K, N, K, false, mxg::kPlain, stream);
 }
 
@@ -293,6 +321,7 @@ int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, v
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(h, s[0].bytes, stream);   // silu(0) 0 = +0
+    if (mx_few_rows(M)) return mx_matvec(d, x, wq, scales, h, M, 2 * N2, K, true, stream);
     return mx_gemm(d, x, wq, scales, nullptr, h, M, 2 * N2, K, 2 * N2, K, false, mxg::kGated, stream);
 }
 

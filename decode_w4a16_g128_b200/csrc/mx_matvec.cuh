@@ -1,0 +1,205 @@
+// mx_matvec.cuh - few rows of x (decode) times MXFP4 weights: y = x W^T, or silu(gate) up over rows
+// interleaved in blocks of eight.
+//
+// Mathematics: the codes become BF16 with their scale applied, exactly, so that mma.sync m16n8k16 (codes
+// as A: 16 weight rows x 16 k; x as B: 16 k x 8 rows of x) sums exact products in FP32 over all of K.
+//
+// Lane (g, t) = (lane / 4, lane % 4) owns block 4 c + t of rows g and g + 8 in the c-th group of 128 k:
+// one 16-byte load and one scale byte a row, so a block's factor is one register.  A permutation of k
+// that A and B share leaves the sums alone: a word's codes j and j + 4 lie 16 bits apart and become one
+// BF16 pair by a mask, a multiplication by 2^12 + 2^6 (sign to bit 15, the others to bits 6-8), a mask
+// and the factor; x pairs are matched to that.
+//
+// Split: a CTA owns 16 weight rows (or 32, which halves the reads of x) and its warps contiguous runs
+// of the groups; the warps' sums join in warp order through shared memory, so results repeat.  Loads
+// of D groups are in flight a warp.  Bound: memory latency and L2; the whole weight is one pass.
+#pragma once
+
+#include "mx_gemm.cuh"
+
+namespace w4a16 {
+namespace mxv {
+
+constexpr int kMaxM = 32;
+
+struct Params {
+    const uint16_t *x;        // bf16 [M, K]
+    const uint32_t *wq;       // [N, K/8]
+    const uint8_t *ws;        // [N, K/32]
+    uint16_t *out;            // bf16 [M, N], or [M, N/2] (gated)
+    int M, N, K;
+    int gated;
+};
+
+// Codes j and j + 4 of every word -> BF16 pairs times the factor.
+__device__ __forceinline__ void expand_pairs(uint32_t v, const mxg::Factor &s, uint32_t (&r)[4]) {
+    const uint32_t u = v >> 8;
+    r[0] = (v & 0x000F000Fu) * 0x1040u;
+    r[1] = (v & 0x00F000F0u) * 0x0104u;
+    r[2] = (u & 0x000F000Fu) * 0x1040u;
+    r[3] = (u & 0x00F000F0u) * 0x0104u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i] & 0x81C081C0u, s.f);
+    if (s.more) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i], s.more);
+    }
+}
+
+template <int RB>
+struct Codes {
+    uint4 c[RB][2];           // rows g and g + 8 of each row block
+    uint32_t e[RB][2];
+};
+
+template <int RB>
+__device__ __forceinline__ void load_codes(Codes<RB> &st, const Params &p, int group, int row0, int g, int t) {
+    const int blk = 4 * group + t, ks = p.K / mx::kBlock;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = row0 + 16 * rb + g + 8 * h;
+            const bool live = r < p.N && blk < ks;
+            const long long at = static_cast<long long>(live ? r : 0) * ks + (live ? blk : 0);
+            st.c[rb][h] = make_uint4(0u, 0u, 0u, 0u);
+            st.e[rb][h] = 127u;
+            if (live) {
+                st.c[rb][h] = ldg_nc_v4(p.wq + 4 * at);
+                st.e[rb][h] = __ldg(p.ws + at);
+            }
+        }
+}
+
+// 32 values of x rows 8 nb + g.
+template <int NB>
+struct Rows {
+    uint4 v[NB][4];
+};
+template <int NB>
+__device__ __forceinline__ void load_rows(Rows<NB> &st, const Params &p, int group, int g, int t) {
+    const int blk = 4 * group + t;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int m = 8 * nb + g;
+        const bool live = m < p.M && blk < p.K / mx::kBlock;
+        const uint16_t *src = p.x + static_cast<long long>(live ? m : 0) * p.K + (live ? blk : 0) * mx::kBlock;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st.v[nb][q] = live ? ldg_v4(src + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+    return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
+}
+
+template <int RB, int NB>
+__device__ __forceinline__ void multiply(const Codes<RB> &st, const Rows<NB> &x, float (&acc)[RB][NB][2][4]) {
+    mxg::Factor f[RB][2];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) f[rb][h] = mxg::factor_of(st.e[rb][h]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t b[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const uint4 &v = x.v[nb][w];
+            b[nb][0] = prmt(v.x, v.z, 0x5410u);     // k 0 and 4
+            b[nb][1] = prmt(v.x, v.z, 0x7632u);     // 1 and 5
+            b[nb][2] = prmt(v.y, v.w, 0x5410u);
+            b[nb][3] = prmt(v.y, v.w, 0x7632u);
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            uint32_t lo[4], hi[4];
+            expand_pairs(word_of(st.c[rb][0], w), f[rb][0], lo);
+            expand_pairs(word_of(st.c[rb][1], w), f[rb][1], hi);
+            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                mma_bf16_16816(acc[rb][nb][0], a0, b[nb][0], b[nb][1], acc[rb][nb][0]);
+                mma_bf16_16816(acc[rb][nb][1], a1, b[nb][2], b[nb][3], acc[rb][nb][1]);
+            }
+        }
+    }
+}
+
+template <int RB, int NB, int WARPS, int D>
+__global__ void __launch_bounds__(32 * WARPS) matvec_kernel(const Params p) {
+    __shared__ float red[WARPS][RB][16][8 * NB + 1];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int row0 = static_cast<int>(blockIdx.x) * 16 * RB;
+    const int G = (p.K + 127) / 128;
+    const int ga = static_cast<int>(static_cast<long long>(warp) * G / WARPS);
+    const int gb = static_cast<int>(static_cast<long long>(warp + 1) * G / WARPS);
+    float acc[RB][NB][2][4];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[rb][nb][0][i] = acc[rb][nb][1][i] = 0.f;
+    Codes<RB> st[D];
+    Rows<NB> x[NB == 1 ? D : 1];
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (ga + j < gb) {
+            load_codes<RB>(st[j], p, ga + j, row0, g, t);
+            if constexpr (NB == 1) load_rows<NB>(x[j], p, ga + j, g, t);
+        }
+    for (int gi = ga; gi < gb; gi += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            const int group = gi + j;
+            if (group >= gb) break;
+            if constexpr (NB > 1) load_rows<NB>(x[0], p, group, g, t);
+            multiply<RB, NB>(st[j], x[NB == 1 ? j : 0], acc);
+            if (group + D < gb) {
+                load_codes<RB>(st[j], p, group + D, row0, g, t);
+                if constexpr (NB == 1) load_rows<NB>(x[j], p, group + D, g, t);
+            }
+        }
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float(&a)[2][4] = acc[rb][nb];
+            red[warp][rb][g][8 * nb + 2 * t] = a[0][0] + a[1][0];
+            red[warp][rb][g][8 * nb + 2 * t + 1] = a[0][1] + a[1][1];
+            red[warp][rb][g + 8][8 * nb + 2 * t] = a[0][2] + a[1][2];
+            red[warp][rb][g + 8][8 * nb + 2 * t + 1] = a[0][3] + a[1][3];
+        }
+    __syncthreads();
+    if (!p.gated) {
+        for (int i = threadIdx.x; i < 16 * RB * p.M; i += 32 * WARPS) {
+            const int m = i / (16 * RB), r = i % (16 * RB), row = row0 + r;
+            if (row >= p.N) continue;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) v += red[w][r / 16][r % 16][m];
+            p.out[static_cast<long long>(m) * p.N + row] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        }
+    } else {
+        for (int i = threadIdx.x; i < 8 * RB * p.M; i += 32 * WARPS) {
+            const int m = i / (8 * RB), r = i % (8 * RB), row = row0 / 2 + r;
+            if (row >= p.N / 2) continue;
+            float gate = 0.f, up = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                gate += red[w][r / 8][r % 8][m];
+                up += red[w][r / 8][r % 8 + 8][m];
+            }
+            p.out[static_cast<long long>(m) * (p.N / 2) + row] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(mx::gated(gate, up)));
+        }
+    }
+}
+
+}  // namespace mxv
+}  // namespace w4a16

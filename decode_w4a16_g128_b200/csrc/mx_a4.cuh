@@ -93,12 +93,12 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int m, int n, uint32_t id) {
 
 // Bytes first .. first + 15 (blocks of K) of a stored row of ks scale bytes, 127 behind its end and
 // for rows outside.  One 16-byte load where rows are 16-byte aligned; else five aligned words, shifted
-// into place.  A word that sticks out of the whole array (its first or last one) is read by bytes.
-__device__ __forceinline__ uint32_t word_inside(const uint8_t *at, const uint8_t *begin, const uint8_t *end) {
-    if (at >= begin && at + 4 <= end) return __ldg(reinterpret_cast<const uint32_t *>(at));
+// into place (the array starts on a 16-byte boundary; its last word may be cut off: read by bytes).
+__device__ __forceinline__ uint32_t word_inside(const uint8_t *at, const uint8_t *end) {
+    if (at + 4 <= end) return __ldg(reinterpret_cast<const uint32_t *>(at));
     uint32_t v = 0;
-    for (int i = 0; i < 4; ++i)
-        if (at + i >= begin && at + i < end) v |= static_cast<uint32_t>(__ldg(at + i)) << (8 * i);
+    for (int i = 0; i < 3; ++i)
+        if (at + i < end) v |= static_cast<uint32_t>(__ldg(at + i)) << (8 * i);
     return v;
 }
 __device__ __forceinline__ uint4 scale16(const uint8_t *s, int rows, int ks, int row, int first, bool aligned) {
@@ -110,7 +110,7 @@ __device__ __forceinline__ uint4 scale16(const uint8_t *s, int rows, int ks, int
     const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 3u);
     uint32_t w[5], v[4];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = word_inside(at - off + 4 * i, s, end);
+    for (int i = 0; i < 5; ++i) w[i] = word_inside(at - off + 4 * i, end);
     const int valid = ks - first;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -127,7 +127,7 @@ template <int GROUPS, typename Row0>
 __device__ __forceinline__ void load_scales(const uint8_t *s, int rows, int K, int first, int step_t, int tiles, int steps,
                                             uint32_t dst0, uint64_t *empty, uint32_t ready_l, int lane, Row0 row0) {
     const int ks = K / mx::kBlock;
-    const bool aligned = ks % 16 == 0 && (reinterpret_cast<uintptr_t>(s) & 15u) == 0;
+    const bool aligned = ks % 16 == 0;
     Ring st;
     long long issued = 0;
     for (int t = first; t < tiles; t += step_t) {
@@ -175,7 +175,7 @@ __device__ __forceinline__ void load_scales(const uint8_t *s, int rows, int K, i
 
 // ------------------------------------------------------------------ the kernel
 
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     a4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);

@@ -16,7 +16,6 @@ constexpr int64_t kSizeLimit = int64_t(1) << 31;
 struct Span {
     const void *p;
     size_t bytes;
-    bool aligned = true;   // false: any address (scale bytes)
 };
 
 // Every buffer present and aligned, no output on top of another buffer.  The first `outputs`
@@ -25,7 +24,7 @@ int check_buffers(const Span *s, int n, int outputs) {
     for (int i = 0; i < n; ++i)
         if (!s[i].p && s[i].bytes) return W4A16_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i)
-        if (s[i].aligned && s[i].bytes && !aligned16(s[i].p)) return W4A16_ERR_MISALIGNED;
+        if (s[i].bytes && !aligned16(s[i].p)) return W4A16_ERR_MISALIGNED;
     for (int i = 0; i < outputs; ++i)
         for (int j = i + 1; j < n; ++j)
             if (s[i].bytes && s[j].bytes && overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return W4A16_ERR_INVALID_ARG;
@@ -38,6 +37,15 @@ int mx_sizes(int64_t M, int64_t N, int64_t K) {
     return W4A16_OK;
 }
 
+cudaLaunchAttribute mx_cluster(int ctas) {
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = ctas;
+    a.val.clusterDim.y = 1;
+    a.val.clusterDim.z = 1;
+    return a;
+}
+
 int mx_device(DeviceInfo **d) {
     int dev = 0;
     int rc = current_device(&dev);
@@ -48,6 +56,16 @@ int mx_device(DeviceInfo **d) {
         e = cudaFuncSetAttribute(mxg::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mx4::a4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mx4::kSmemBytes);
+    for (int S = 1; S <= mxg::kMaxSplits && e == cudaSuccess; S *= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * S, 1, 1);
+        cfg.blockDim = dim3(mxg::kThreads, 1, 1);
+        cfg.dynamicSmemBytes = mxg::kSmemBudget;
+        cudaLaunchAttribute cl = mx_cluster(2 * S);
+        cfg.attrs = &cl;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[S], mxg::gemm_kernel<true>, &cfg);
+    }
     if (e != cudaSuccess) return cuda_fail(e);
     (*d)->mx_ready = true;
     return W4A16_OK;
@@ -58,20 +76,21 @@ int zero_fill(void *p, size_t bytes, void *stream) {
     return e == cudaSuccess ? W4A16_OK : cuda_fail(e);
 }
 
-// A launch with the programmatic-dependent-launch attribute (every kernel here waits for the
-// preceding one before its first access).
+// A launch of clusters of `cluster` CTAs with the programmatic-dependent-launch attribute (every
+// kernel here waits for the preceding one before its first access).
 template <typename... KArgs, typename... Args>
-int mx_launch(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, void *stream, Args... args) {
+int mx_launch(void (*kernel)(KArgs...), dim3 grid, int cluster, int block, size_t smem, void *stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1] = mx_cluster(cluster);
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e == cudaSuccess ? W4A16_OK : cuda_fail(e);
 }
@@ -88,19 +107,30 @@ mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilo
     return o;
 }
 
-// Outputs of a CTA pair: the width with the least estimated time, rounds of the persistent grid times
-// the SM cycles of a stage (four MMAs of 256 rows, or the expanding of half of the outputs' codes).
-int mx_gemm_width(int64_t M, int64_t J, bool backward, int pairs) {
-    const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows);
-    int best = 0;
+// Outputs of a CTA pair (bn) and pairs that share a tile's contraction (splits): the least estimated
+// time in SM cycles.  A stage takes its eight MMAs (half a cycle an output, and about 52 cycles
+// at least) or the expanding of a CTA's codes; a persistent grid runs rounds of tiles, a split one has
+// to fit the device at once and pays for the exchange of sums.
+struct MxShape {
+    int bn = 0, splits = 1;
+};
+MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, const DeviceInfo *d) {
+    const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows), steps = (C + mxg::kStep - 1) / mxg::kStep;
+    MxShape best;
     int64_t cost = 0;
-    for (int bn = 64; bn <= (backward ? 320 : 256); bn += backward ? 64 : 32) {
-        const int64_t tiles = tm * ((J + bn - 1) / bn), rounds = (tiles + pairs - 1) / pairs;
-        const int64_t mma = bn <= 256 ? std::max(bn / 2, 52) : 128 + std::max((bn - 256) / 2, 52);
-        const int64_t c = rounds * std::max<int64_t>(4 * mma, 256);
-        if (!best || c <= cost) {
-            best = bn;
-            cost = c;
+    for (int bn = 64; bn <= mxg::kMaxBN; bn += backward ? 64 : 32) {
+        const int64_t tiles = tm * ((J + bn - 1) / bn);
+        const int64_t mma = 8 * std::max(bn / 2, 52) + 60, stage = std::max<int64_t>(mma, 400 + bn);
+        for (int S = 1; S <= mxg::kMaxSplits; S *= 2) {
+            const int64_t room = std::min<int64_t>(d->mx_clusters[S], d->sms / (2 * S));
+            if (S > 1 && (tiles > room || steps < 2 * S)) continue;
+            const int64_t rounds = S > 1 ? 1 : (tiles + room - 1) / room;
+            const int64_t c = rounds * ((steps + S - 1) / S) * stage + (S > 1 ? 1500 : 0);
+            if (!best.bn || c <= cost) {
+                best.bn = bn;
+                best.splits = S;
+                cost = c;
+            }
         }
     }
     return best;
@@ -109,24 +139,24 @@ int mx_gemm_width(int64_t M, int64_t J, bool backward, int pairs) {
 // D = A . W^T (forward) or A . W (backward) on the tensor cores: A bf16 [M, C], J outputs.
 int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws, const void *dh, void *out, int64_t M,
             int64_t J, int64_t C, int64_t N, int64_t K, bool backward, int epilogue, void *stream) {
-    const int pairs = d->sms / 2;
+    const MxShape shape = mx_gemm_shape(M, J, C, backward, d);
     mxg::Params p;
     p.o = mx_output(out, dh, M, J, epilogue);
     p.ws = ws;
     p.C = static_cast<int>(C);
     p.ks = static_cast<int>(K / mx::kBlock);
-    p.bn = mx_gemm_width(M, J, backward, pairs);
+    p.bn = shape.bn;
+    p.splits = shape.splits;
     const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows), tiles = tm * ((J + p.bn - 1) / p.bn);
     if (tiles >= kSizeLimit) return W4A16_ERR_UNSUPPORTED;
     p.tiles_m = static_cast<int>(tm);
     p.tiles = static_cast<int>(tiles);
     const int half = p.bn / 2;
-    p.b_bytes = backward ? (half + 63) / 64 * 8192 : half * 128;
-    p.w_bytes = backward ? 32 * half : 128 * half;
-    p.w_slots = backward ? 8 : 3;
-    p.w_pitch = backward ? half / 2 : 128;
-    // codes tile: rows of 32, 64 and 128 bytes are swizzled by the copy (else neighbouring rows'
-    // 16-byte chunks would share banks); chunks at a pitch of 48 or 80 bytes spread by themselves
+    p.b_bytes = backward ? (half + 63) / 64 * mxg::kGroupBytes : half * mxg::kStep * 2;
+    p.w_bytes = half * mxg::kStep / 2;
+    p.w_pitch = backward ? half / 2 : mxg::kStep / 2;
+    // codes tile: rows of 32 and 64 bytes are swizzled by the copy (else neighbouring rows' 16-byte
+    // chunks would share banks); chunks at a pitch of 16 or 48 bytes spread by themselves
     CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE;
     p.w_swz_shift = p.w_swz_mask = 0;
     if (p.w_pitch == 32) {
@@ -137,23 +167,19 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
         swz = CU_TENSOR_MAP_SWIZZLE_64B;
         p.w_swz_shift = 1;
         p.w_swz_mask = 3;
-    } else if (p.w_pitch == 128) {
-        swz = CU_TENSOR_MAP_SWIZZLE_128B;
     }
-    p.stages = mxg::kMaxStages;
-    while (mxg::smem_bytes(p.stages, p.b_bytes, p.w_slots, p.w_bytes) > mxg::kSmemBudget) --p.stages;
-    p.scales16 = p.ks % 16 == 0 && aligned16(ws);
-    const int smem = mxg::smem_bytes(p.stages, p.b_bytes, p.w_slots, p.w_bytes);
+    const int smem = mxg::smem_bytes(p.b_bytes, p.w_bytes);
 
     CUtensorMap tx, tw;
-    int rc = encode_2d(d, &tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a, C, M, C * 2, mxg::kStep, mxg::kRows,
-                       CU_TENSOR_MAP_SWIZZLE_128B);
+    int rc = encode_2d(d, &tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a, C, M, C * 2, 64, mxg::kRows, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
-    rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : 32, backward ? mxg::kStep : half, swz);
+    rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : mxg::kStep / 8,
+                   backward ? mxg::kStep : half, swz);
     if (rc) return rc;
-    const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)), 1, 1);
+    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, d->mx_clusters[1]);
+    const dim3 grid(static_cast<unsigned>(2 * p.splits * clusters), 1, 1);
     const auto kernel = backward ? mxg::gemm_kernel<true> : mxg::gemm_kernel<false>;
-    return mx_launch(kernel, grid, mxg::kThreads, smem, stream, tx, tw, p);
+    return mx_launch(kernel, grid, 2 * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
 }
 
 // Outputs of a CTA pair of the 4-bit product: the fewest column-rounds of the persistent grid; an MMA
@@ -194,7 +220,7 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
                    CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
     const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)), 1, 1);
-    return mx_launch(mx4::a4_kernel, grid, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, p);
+    return mx_launch(mx4::a4_kernel, grid, 2, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, p);
 }
 
 // Few rows of x: forward products alone.
@@ -203,7 +229,7 @@ bool mx_few_rows(int64_t M) { return M <= mxv::kMaxM; }
 template <int RB, int NB, int WARPS, int D>
 int mx_matvec_launch(const mxv::Params &p, void *stream) {
     const dim3 grid(static_cast<unsigned>((int64_t(p.N) + 16 * RB - 1) / (16 * RB)), 1, 1);
-    return mx_launch(mxv::matvec_kernel<RB, NB, WARPS, D>, grid, 32 * WARPS, 0, stream, p);
+    return mx_launch(mxv::matvec_kernel<RB, NB, WARPS, D>, grid, 1, 32 * WARPS, 0, stream, p);
 }
 
 int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *ws, void *out, int64_t M, int64_t N,
@@ -239,7 +265,7 @@ int w4a16_mx_quantize(const void *w, int32_t w_dtype, uint32_t *wq, uint8_t *sca
     int rc = mx_sizes(0, N, K);
     if (rc || N == 0 || K == 0) return rc;
     const size_t n = size_t(N) * K;
-    const Span s[3] = {{wq, n / 2}, {scales, n / 32, false}, {w, n * (w_dtype == W4A16_DTYPE_F32 ? 4 : 2)}};
+    const Span s[3] = {{wq, n / 2}, {scales, n / 32}, {w, n * (w_dtype == W4A16_DTYPE_F32 ? 4 : 2)}};
     rc = check_buffers(s, 3, 2);
     if (rc) return rc;
     std::lock_guard<std::mutex> lock(g_mu);
@@ -249,8 +275,8 @@ int w4a16_mx_quantize(const void *w, int32_t w_dtype, uint32_t *wq, uint8_t *sca
     const long long words = N * (K / 8);
     const dim3 grid(stream_grid(words, d->sms), 1, 1);
     if (w_dtype == W4A16_DTYPE_BF16)
-        return mx_launch(mx::quantize_kernel<true>, grid, mx::kQThreads, 0, stream, w, wq, scales, words);
-    return mx_launch(mx::quantize_kernel<false>, grid, mx::kQThreads, 0, stream, w, wq, scales, words);
+        return mx_launch(mx::quantize_kernel<true>, grid, 1, mx::kQThreads, 0, stream, w, wq, scales, words);
+    return mx_launch(mx::quantize_kernel<false>, grid, 1, mx::kQThreads, 0, stream, w, wq, scales, words);
 }
 
 int w4a16_mx_dequantize(const uint32_t *wq, const uint8_t *scales, void *w, int32_t w_dtype, int64_t N, int64_t K,
@@ -259,7 +285,7 @@ int w4a16_mx_dequantize(const uint32_t *wq, const uint8_t *scales, void *w, int3
     int rc = mx_sizes(0, N, K);
     if (rc || N == 0 || K == 0) return rc;
     const size_t n = size_t(N) * K;
-    const Span s[3] = {{w, n * (w_dtype == W4A16_DTYPE_F32 ? 4 : 2)}, {wq, n / 2}, {scales, n / 32, false}};
+    const Span s[3] = {{w, n * (w_dtype == W4A16_DTYPE_F32 ? 4 : 2)}, {wq, n / 2}, {scales, n / 32}};
     rc = check_buffers(s, 3, 1);
     if (rc) return rc;
     std::lock_guard<std::mutex> lock(g_mu);
@@ -269,8 +295,8 @@ int w4a16_mx_dequantize(const uint32_t *wq, const uint8_t *scales, void *w, int3
     const long long words = N * (K / 8);
     const dim3 grid(stream_grid(words, d->sms), 1, 1);
     if (w_dtype == W4A16_DTYPE_BF16)
-        return mx_launch(mx::dequantize_kernel<true>, grid, mx::kQThreads, 0, stream, wq, scales, w, words);
-    return mx_launch(mx::dequantize_kernel<false>, grid, mx::kQThreads, 0, stream, wq, scales, w, words);
+        return mx_launch(mx::dequantize_kernel<true>, grid, 1, mx::kQThreads, 0, stream, wq, scales, w, words);
+    return mx_launch(mx::dequantize_kernel<false>, grid, 1, mx::kQThreads, 0, stream, wq, scales, w, words);
 }
 
 int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, void *y, int64_t M, int64_t N, int64_t K,
@@ -278,7 +304,7 @@ int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, vo
     int rc = mx_sizes(M, N, K);
     if (rc || M == 0 || N == 0) return rc;
     const size_t nw = size_t(N) * K;
-    const Span s[4] = {{y, size_t(M) * N * 2}, {x, size_t(M) * K * 2}, {wq, nw / 2}, {scales, nw / 32, false}};
+    const Span s[4] = {{y, size_t(M) * N * 2}, {x, size_t(M) * K * 2}, {wq, nw / 2}, {scales, nw / 32}};
     rc = check_buffers(s, 4, 1);
     if (rc) return rc;
     std::lock_guard<std::mutex> lock(g_mu);
@@ -295,7 +321,7 @@ int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_
     int rc = mx_sizes(M, N, K);
     if (rc || M == 0 || N == 0) return rc;
     const size_t nx = size_t(M) * K, nw = size_t(N) * K;
-    const Span s[5] = {{y, size_t(M) * N * 2}, {xq, nx / 2}, {xscales, nx / 32, false}, {wq, nw / 2}, {scales, nw / 32, false}};
+    const Span s[5] = {{y, size_t(M) * N * 2}, {xq, nx / 2}, {xscales, nx / 32}, {wq, nw / 2}, {scales, nw / 32}};
     rc = check_buffers(s, 5, 1);
     if (rc) return rc;
     std::lock_guard<std::mutex> lock(g_mu);
@@ -313,7 +339,7 @@ int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, v
     if (N2 % 8 != 0 || N2 >= kSizeLimit / 2) return W4A16_ERR_UNSUPPORTED;
     if (M == 0 || N2 == 0) return W4A16_OK;
     const size_t nw = size_t(N2) * 2 * K;
-    const Span s[4] = {{h, size_t(M) * N2 * 2}, {x, size_t(M) * K * 2}, {wq, nw / 2}, {scales, nw / 32, false}};
+    const Span s[4] = {{h, size_t(M) * N2 * 2}, {x, size_t(M) * K * 2}, {wq, nw / 2}, {scales, nw / 32}};
     rc = check_buffers(s, 4, 1);
     if (rc) return rc;
     std::lock_guard<std::mutex> lock(g_mu);
@@ -332,7 +358,7 @@ int w4a16_mx_matmul_backward(const void *dy, const uint32_t *wq, const uint8_t *
     if (N % 8 != 0) return W4A16_ERR_UNSUPPORTED;
     if (M == 0 || K == 0) return W4A16_OK;
     const size_t nw = size_t(N) * K;
-    const Span s[4] = {{dx, size_t(M) * K * 2}, {dy, size_t(M) * N * 2}, {wq, nw / 2}, {scales, nw / 32, false}};
+    const Span s[4] = {{dx, size_t(M) * K * 2}, {dy, size_t(M) * N * 2}, {wq, nw / 2}, {scales, nw / 32}};
     rc = check_buffers(s, 4, 1);
     if (rc) return rc;
     std::lock_guard<std::mutex> lock(g_mu);
@@ -351,7 +377,7 @@ int w4a16_mx_gate_up_backward(const void *x, const uint32_t *wq, const uint8_t *
     if (M == 0) return W4A16_OK;
     const size_t nw = size_t(N2) * 2 * K;
     const Span s[6] = {{dx, size_t(M) * K * 2},  {dgu, size_t(M) * N2 * 4}, {x, size_t(M) * K * 2},
-                       {dh, size_t(M) * N2 * 2}, {wq, nw / 2},              {scales, nw / 32, false}};
+                       {dh, size_t(M) * N2 * 2}, {wq, nw / 2},              {scales, nw / 32}};
     rc = check_buffers(s, 6, 2);
     if (rc) return rc;
     std::lock_guard<std::mutex> lock(g_mu);

@@ -7,21 +7,26 @@
 // scale is applied before the product, no factor is left for the accumulator) and the tensor cores'
 // products are exact in FP32; the sum over all of the contraction stays in tensor memory.
 //
-// A CTA pair (cta_group::2) computes 256 rows x BN outputs, K = 64 of the contraction a stage:
-//   A  128 rows x 64 of x per CTA, by TMA, K-major, 128-byte swizzle;
-//   B  each CTA expands its BN / 2 outputs' codes into BF16 in shared memory.  Forward: [output][64 k],
-//      K-major.  Backward: the stored rows run along the outputs, so the tile is kept as stored,
-//      [64 n][64 outputs] per group of 64 outputs, MN-major: the transposition is the descriptor's.
-//      BN > 256 (backward) is a second MMA over the outputs behind the first 128 of each CTA.
-// Accumulators fill tensor memory: two of BN <= 256 columns (the epilogue of a tile runs under the
-// next tile's main loop), or one wider.  The grid is persistent; the host picks BN for the fewest
-// column-rounds (see mx_entry.cuh).
+// A CTA pair (cta_group::2) computes 256 rows x BN <= 256 outputs, K = 128 of the contraction a stage:
+//   A  128 rows of x per CTA, by TMA, K-major, two tiles of 64 k with the 128-byte swizzle;
+//   B  each CTA expands its BN / 2 outputs' codes into BF16 in shared memory.  Forward: [output][64 k]
+//      twice, K-major.  Backward: the stored rows run along the outputs, so the tile is kept as stored,
+//      [128 n][64 outputs] per group of 64 outputs, MN-major: the transposition is the descriptor's.
+// Two accumulators of 256 columns fill tensor memory: the epilogue of a tile runs under the next
+// tile's main loop.  The grid is persistent; the host picks BN for the fewest column-rounds (see
+// mx_entry.cuh).  Where the tiles leave SMs idle, S pairs share a tile (a cluster of 2 S CTAs), each a
+// run of the stages; their partial sums meet in shared memory over the cluster, added in split order.
 //
-// Roles (512 threads): warp 0 x by TMA, warp 1 MMA issue (leader) and tensor memory, warp 2 codes by
-// TMA, warp 3 of the peer forwards "expanded" to the leader, warps 4-7 epilogue, warps 8-15 expand
-// codes.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's two expanding warps, the
-// peer's forwarder), empty[s] (both CTAs; the stage's MMAs completed), exp[s] (peer: its two
-// expanding warps), w_full / w_empty (codes ring), acc_full / acc_empty (accumulators).
+// Roles (768 threads): warp 1 MMA issue (leader) and tensor memory, warps 4-7 epilogue, twelve of warps
+// 8-23 expand codes in three teams, and beside warp 1 on its scheduler one warp that copies codes, one
+// that copies x, and the peer's that forwards "expanded" to the leader.  The ring has three stages, one
+// a team.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's four expanding warps, the peer's
+// forwarder), empty[s] (both CTAs; the stage's MMAs completed), exp[s] (peer: its four expanding
+// warps), w_full[s] / w_empty[s] (codes), acc_full / acc_empty (accumulators).
+//
+// What the stage's length and the roles' places were measured to be worth (2048 x 9728 x 2560, forward):
+// the MMAs of K = 64 a stage take less time than the dozens of instructions around a stage's waits
+// do in a crowded SM, and the tensor pipe idles meanwhile.
 #pragma once
 
 #include "mx.cuh"
@@ -29,28 +34,26 @@
 namespace w4a16 {
 namespace mxg {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kRows = 128;               // x rows of a CTA
-constexpr int kStep = 64;                // contraction of a stage
+constexpr int kStep = 128;               // contraction of a stage
+constexpr int kStages = 3;
 constexpr int kABytes = kRows * kStep * 2;
-constexpr int kMaxStages = 8;
-constexpr int kMaxWSlots = 8;
-// Stages of a codes copy.  A copy costs the TMA unit time per row, whatever the row's length (a copy
-// of 128 rows x 32 bytes a stage, beside x's 128 rows, held the whole pipeline to about 800 cycles
-// a stage): forward rows are fetched 128 bytes at a time, K = 256, for the four teams' stages.
-template <bool BACKWARD>
-constexpr int kWSpan = BACKWARD ? 1 : 4;
-constexpr int kDeqWarps = 8, kDeqThreads = 32 * kDeqWarps, kEpiWarps = 4;
+constexpr int kEpiWarps = 4;
+constexpr int kTeams = kStages, kTeamWarps = 4;   // expanding warps, see there
+constexpr int kMaxSplits = 4;
+// Warps with w % 4 == 1 share the issuing warp's scheduler: light roles.
+constexpr int kWarpMma = 1, kWarpCodes = 9, kWarpX = 13, kWarpForward = 17;
 constexpr int kTmemCols = 512;
-constexpr int kMaxBN = 320;              // outputs of a pair (forward: 256)
-constexpr int kBarBytes = 512;
+constexpr int kMaxBN = 256;              // outputs of a pair
+constexpr int kBarBytes = 256;
 constexpr int kSmemBudget = 227 * 1024;
-constexpr int kTeams = 4, kTeamWarps = kDeqWarps / kTeams;   // expanding warps, see there
 
-// Dynamic shared memory: stages x (A, B), codes ring, barriers, and slack for 1024-byte alignment.
-__host__ __device__ constexpr int smem_bytes(int stages, int b_bytes, int w_slots, int w_bytes) {
-    return stages * (kABytes + b_bytes) + w_slots * w_bytes + kBarBytes + 1024;
+// Dynamic shared memory: stages of (A, B, codes), barriers, and slack for 1024-byte alignment.
+__host__ __device__ constexpr int smem_bytes(int b_bytes, int w_bytes) {
+    return kStages * (kABytes + b_bytes + w_bytes) + kBarBytes + 1024;
 }
+static_assert(smem_bytes(kMaxBN / 2 * kStep * 2, kMaxBN / 2 * kStep / 2) <= kSmemBudget, "shared memory budget");
 
 // ------------------------------------------------------------------ PTX
 
@@ -77,11 +80,12 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc,
 }
 
 // Descriptor of an MN-major operand, 128-byte swizzle: rows of 64 contiguous outputs (128 bytes), 8
-// rows of the contraction 1024 bytes apart (stride offset), groups of 64 outputs 8192 bytes apart
+// rows of the contraction 1024 bytes apart (stride offset), groups of 64 outputs kGroupBytes apart
 // (leading offset).
+constexpr int kGroupBytes = kStep * 128;
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr) {
     uint64_t d = static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(8192 >> 4) << 16;
+    d |= static_cast<uint64_t>(kGroupBytes >> 4) << 16;
     d |= static_cast<uint64_t>(1024 >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
@@ -97,37 +101,27 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// A scale byte as up to two BF16 factors: a code's three low bits in BF16's lowest exponent bits
-// and highest mantissa bit are its magnitude times 2^-126 (code 1 as a subnormal), so the factor is
-// 2^(e - 1); above e = 128 that is beyond BF16 and the rest, 2^(e - 128), comes as a second one.
-struct Factor {
-    uint32_t f, more;          // pairs; more = 0: none
-};
-__device__ __forceinline__ Factor factor_of(uint32_t e) {
-    Factor r;
-    r.f = ((e < 128u ? e : 128u) + 126u) * 0x00800080u;
-    r.more = 0;
-    if (e > 128u) {
-        r.more = e == mx::kScaleNan ? 0x7FC07FC0u : (e - 1u) * 0x00800080u;
-    }
-    return r;
+// A scale byte as BF16 factors: a code's three low bits in BF16's lowest exponent bits and highest
+// mantissa bit are its magnitude times 2^-126 (code 1 as a subnormal), so the factor is 2^(e - 1).
+// Above e = 128 that is beyond BF16: there the factor is 2^127, and the rest, 2^(e - 128) or NaN, a
+// second one.
+constexpr uint32_t kOneFactor = 128;       // largest scale byte with one factor
+__device__ __forceinline__ uint32_t factor_of(uint32_t e) { return e * 0x00800080u + 126u * 0x00800080u; }
+__device__ __forceinline__ uint32_t second_factor_of(uint32_t e) {
+    return e == mx::kScaleNan ? 0x7FC07FC0u : (e - 1u) * 0x00800080u;
 }
 
-// Eight codes, lowest k first -> four BF16 pairs, lowest k first.  Codes 2i and 2i + 1 go to the two
-// halves of a register (the selector's sign-replicating bytes are zero there: every byte is below
-// 128), one multiplication by 2^12 + 2^6 puts the sign bit to bit 15 and the others to bits 6-8.
-__device__ __forceinline__ void expand8(uint32_t v, const Factor &s, uint32_t (&r)[4]) {
+// Eight codes, lowest k first -> four BF16 pairs, lowest k first, times the factor.  Codes 2i and 2i + 1
+// go to the two halves of a register (the selector's sign-replicating bytes are zero there: every byte
+// is below 128), one multiplication by 2^12 + 2^6 puts the sign bit to bit 15 and the others to bits 6-8.
+__device__ __forceinline__ void expand8(uint32_t v, uint32_t f, uint32_t (&r)[4]) {
     const uint32_t lo = v & 0x0F0F0F0Fu, hi = (v >> 4) & 0x0F0F0F0Fu;
     r[0] = prmt(lo, hi, 0xC480u);
     r[1] = prmt(lo, hi, 0xD591u);
     r[2] = prmt(lo, hi, 0xE6A2u);
     r[3] = prmt(lo, hi, 0xF7B3u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2((r[i] * 0x1040u) & 0x81C081C0u, s.f);
-    if (s.more) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], s.more);
-    }
+    for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2((r[i] * 0x1040u) & 0x81C081C0u, f);
 }
 
 // ------------------------------------------------------------------ epilogue helpers
@@ -218,12 +212,10 @@ struct Params {
     int ks;                   // scale bytes of a row of W (K / 32)
     int bn;                   // outputs of a pair
     int tiles_m, tiles;
-    int stages;
-    int b_bytes, w_bytes;     // B tile of a CTA and stage, codes of a copy
-    int w_slots;              // codes ring
+    int b_bytes, w_bytes;     // B tile and codes of a CTA and stage
     int w_pitch;              // bytes of a codes tile row
     int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
-    int scales16;             // rows of scale bytes start on 16-byte boundaries
+    int splits;               // pairs that share a tile (the grid then has one cluster a tile)
 };
 
 struct Ring {
@@ -237,77 +229,103 @@ struct Ring {
     }
 };
 
-// ------------------------------------------------------------------ scale bytes of a team's stages
+// ------------------------------------------------------------------ scale bytes
 
-// Forward, stage i of team i % 4 with i % 8 < 4: what scale_bytes needs of row j for stages i and i + 4;
-// 127 outside W, where the codes are filled with zeros.  One 16-byte load where rows of scale bytes
-// are 16-byte aligned (every lane reads another row, so a load costs a cache line a lane whatever its
-// width), else four bytes.  The words are kept as loaded and looked at two stages later: a look here
-// would wait for the load.
-__device__ __forceinline__ uint4 scale_words(const Params &p, int j, int i, bool live) {
-    uint4 v = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if (!live || j >= p.o.J) return v;
-    const uint8_t *row = p.ws + static_cast<long long>(j) * p.ks;
-    const int b = 2 * i;
-    if (p.scales16) {
-        if ((b & ~15) < p.ks) v = ldg_nc_v4(row + (b & ~15));
-    } else {
-        if (b < p.ks) v.x = __ldg(row + b);
-        if (b + 1 < p.ks) v.y = __ldg(row + b + 1);
-        if (b + 8 < p.ks) v.z = __ldg(row + b + 8);
-        if (b + 9 < p.ks) v.w = __ldg(row + b + 9);
-    }
+// Up to four scale bytes of a stored row from block `blk` on: the aligned words that hold them (the
+// array starts on a 16-byte boundary), kept as loaded and looked at a stage later, since a look here
+// would wait for the load.  The array's last word may be cut off: it is read by bytes then.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t *at, const uint8_t *end) {
+    if (at + 4 <= end) return __ldg(reinterpret_cast<const uint32_t *>(at));
+    uint32_t v = 0;
+    for (int i = 0; i < 3; ++i)
+        if (at + i < end) v |= static_cast<uint32_t>(__ldg(at + i)) << (8 * i);
     return v;
 }
-
-// The bytes of blocks 2i, 2i + 1 (stage i, bits 0-15) and 2i + 8, 2i + 9 (stage i + 4, bits 16-31).
-__device__ __forceinline__ uint32_t scale_bytes(const Params &p, const uint4 &v, int team) {
-    if (p.scales16) {
-        const uint32_t lo = team < 2 ? v.x : v.y, hi = team < 2 ? v.z : v.w;
-        return team & 1 ? prmt(lo, hi, 0x7632u) : prmt(lo, hi, 0x5410u);
+__device__ __forceinline__ uint32_t scale_offset(int row, int blk, int ks) {
+    return (static_cast<uint32_t>(row) * static_cast<uint32_t>(ks) + static_cast<uint32_t>(blk)) & 3u;
+}
+__device__ __forceinline__ uint2 load_scales(const uint8_t *ws, const uint8_t *end, bool live, int row, int blk, int blks,
+                                             int ks) {
+    uint2 v = make_uint2(0u, 0u);
+    if (!live || blk >= ks) return v;
+    const int off = static_cast<int>(scale_offset(row, blk, ks));
+    const uint8_t *at = ws + (static_cast<long long>(row) * ks + blk - off);
+    v.x = scale_word(at, end);
+    if (off + blks > 4) v.y = scale_word(at + 4, end);
+    return v;
+}
+// Those bytes; 127 behind the row's end, where the codes are zeros.
+__device__ __forceinline__ uint32_t scales_of(uint2 v, int row, int blk, int ks) {
+    uint32_t e = __funnelshift_r(v.x, v.y, 8 * scale_offset(row, blk, ks));
+    const int left = ks - blk;
+    if (left < 4) {
+        const uint32_t mask = left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+        e = (e & mask) | (0x7F7F7F7Fu & ~mask);
     }
-    return prmt(prmt(v.x, v.y, 0x0040u), prmt(v.z, v.w, 0x0040u), 0x5410u);
+    return e;
 }
 
-// Backward: the byte of row n, block b.
-__device__ __forceinline__ uint32_t scale_by_column(const Params &p, int n, int b, bool live) {
-    return live && n < p.C && b < p.ks ? __ldg(p.ws + static_cast<long long>(n) * p.ks + b) : 127u;
+// A block of 32 codes -> 64 bytes of BF16 at `to`, the first of four swizzled 16-byte chunks.
+__device__ __forceinline__ void expand_block(const uint4 &c, uint32_t to, uint32_t e) {
+    const uint32_t f = factor_of(min(e, kOneFactor));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    if (e <= kOneFactor) {
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            uint32_t v[4];
+            expand8(w[jj], f, v);
+            sts128(to ^ (jj << 4), make_uint4(v[0], v[1], v[2], v[3]));
+        }
+    } else {
+        const uint32_t more = second_factor_of(e);
+#pragma unroll 1
+        for (int jj = 0; jj < 4; ++jj) {
+            uint32_t v[4];
+            expand8(jj == 0 ? c.x : (jj == 1 ? c.y : (jj == 2 ? c.z : c.w)), f, v);
+            sts128(to ^ (jj << 4), make_uint4(mul_bf16x2(v[0], more), mul_bf16x2(v[1], more), mul_bf16x2(v[2], more),
+                                              mul_bf16x2(v[3], more)));
+        }
+    }
+}
+
+__device__ __forceinline__ void st_dsmem_v4(uint32_t cluster_addr, uint4 v) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
 }
 
 // ------------------------------------------------------------------ the kernel
 
 template <bool BACKWARD>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int stages = p.stages;
-    uint8_t *sa = smem, *sb = sa + stages * kABytes, *sw = sb + stages * p.b_bytes;
-    uint64_t *ready = reinterpret_cast<uint64_t *>(sw + p.w_slots * p.w_bytes);
-    uint64_t *empty = ready + kMaxStages, *expd = empty + kMaxStages;
-    uint64_t *w_full = expd + kMaxStages, *w_empty = w_full + kMaxWSlots;
-    uint64_t *acc_full = w_empty + kMaxWSlots, *acc_empty = acc_full + 2;
+    uint8_t *sa = smem, *sb = sa + kStages * kABytes, *sw = sb + kStages * p.b_bytes;
+    uint64_t *ready = reinterpret_cast<uint64_t *>(sw + kStages * p.w_bytes);
+    uint64_t *empty = ready + kStages, *expd = empty + kStages, *w_full = expd + kStages, *w_empty = w_full + kStages;
+    uint64_t *acc_full = w_empty + kStages, *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
-    static_assert((3 * kMaxStages + 2 * kMaxWSlots + 4) * 8 + 8 <= kBarBytes, "barrier area");
+    static_assert((5 * kStages + 4) * 8 + 8 <= kBarBytes, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t cluster_rank = cluster_ctarank();       // 2 split + rank in the pair
+    const uint32_t rank = cluster_rank & 1u, lead = cluster_rank & ~1u;
     const bool leader = rank == 0;
-    const int steps = (p.C + kStep - 1) / kStep;
+    const int all_steps = (p.C + kStep - 1) / kStep, split = static_cast<int>(cluster_rank >> 1);
+    const int step0 = static_cast<int>(static_cast<long long>(split) * all_steps / p.splits);
+    const int steps = static_cast<int>(static_cast<long long>(split + 1) * all_steps / p.splits) - step0;
     const int half = p.bn / 2;                       // outputs that this CTA expands
-    const int nacc = p.bn <= 256 ? 2 : 1;
-    const int pairs = static_cast<int>(gridDim.x) / 2, first = static_cast<int>(blockIdx.x) / 2;
+    // tiles of this pair: first, first + pairs, ... (one tile with splits)
+    const int pairs = static_cast<int>(gridDim.x) / (2 * p.splits), first = static_cast<int>(blockIdx.x) / (2 * p.splits);
 
     if (threadIdx.x == 0) {
         pdl_launch_dependents();
-        for (int i = 0; i < kMaxStages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&ready[i], 1 + kTeamWarps + 1);
             mbar_init(&empty[i], 1);
             mbar_init(&expd[i], kTeamWarps);
-        }
-        for (int i = 0; i < kMaxWSlots; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kWSpan<BACKWARD> * kTeamWarps);
+            mbar_init(&w_empty[i], kTeamWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -315,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == kWarpMma) {
         tmem_alloc_pair(tmem_slot, kTmemCols);
         tmem_relinquish_pair();
     }
@@ -323,9 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t ready_l = dsmem_addr(smem_u32(ready), 0), acc_empty_l = dsmem_addr(smem_u32(acc_empty), 0);
+    const uint32_t ready_l = dsmem_addr(smem_u32(ready), lead), acc_empty_l = dsmem_addr(smem_u32(acc_empty), lead);
+    const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
 
-    if (warp == 0 && lane == 0) {
+    if (warp == kWarpX && lane == 0) {
         // ---------------------------------------------------------------- x by TMA
         prefetch_tmap(&tm_x);
         pdl_wait();
@@ -335,206 +354,143 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int t = first; t < p.tiles && ok; t += pairs) {
             const int row = (t % p.tiles_m) * 2 * kRows + static_cast<int>(rank) * kRows;
             for (int i = 0; i < steps; ++i) {
-                if (issued >= stages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
+                if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
                 if (leader) mbar_arrive_expect_tx(&ready[st.slot], 2 * kABytes);   // both CTAs' rows
-                tma_load_2d_pair(sa + st.slot * kABytes, &tm_x, ready_l + 8 * st.slot, i * kStep, row);
+                uint8_t *dst = sa + st.slot * kABytes;
+                tma_load_2d_pair(dst, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep, row);
+                tma_load_2d_pair(dst + kABytes / 2, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep + 64, row);
                 ++issued;
-                st.advance(stages);
+                st.advance(kStages);
             }
         }
         // leave no copy in flight: the last stages' MMAs, which consumed them, completed
-        for (long long j = issued > stages ? issued - stages : 0; j < issued; ++j)
-            mbar_wait(&empty[j % stages], static_cast<uint32_t>((j / stages) & 1), false);
-    } else if (warp == 2 && lane == 0) {
+        for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+            mbar_wait(&empty[j % kStages], static_cast<uint32_t>((j / kStages) & 1), false);
+    } else if (warp == kWarpCodes && lane == 0) {
         // ---------------------------------------------------------------- codes by TMA
         prefetch_tmap(&tm_w);
         pdl_wait();
-        const int slots = p.w_slots;
         Ring st;
         long long issued = 0;
         bool ok = true;
         for (int t = first; t < p.tiles && ok; t += pairs) {
             const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
-            for (int i = 0; i < steps; i += kWSpan<BACKWARD>) {
-                if (issued >= slots && !mbar_wait(&w_empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
+            for (int i = 0; i < steps; ++i) {
+                if (issued >= kStages && !mbar_wait(&w_empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
                 mbar_arrive_expect_tx(&w_full[st.slot], p.w_bytes);
                 if constexpr (BACKWARD)
-                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], j0 / 8, i * kStep);
+                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], j0 / 8, (step0 + i) * kStep);
                 else
-                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], i * (kStep / 8), j0);
+                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], (step0 + i) * (kStep / 8), j0);
                 ++issued;
-                st.advance(slots);
+                st.advance(kStages);
             }
         }
-        for (long long j = issued > slots ? issued - slots : 0; j < issued; ++j)
-            mbar_wait(&w_full[j % slots], static_cast<uint32_t>((j / slots) & 1), false);
-    } else if (warp == 3 && lane == 0 && !leader) {
+        for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
+            mbar_wait(&w_full[j % kStages], static_cast<uint32_t>((j / kStages) & 1), false);
+    } else if (warp == kWarpForward && lane == 0 && !leader) {
         // ---------------------------------------------------------------- "expanded", to the leader
+        // The arrival has the default (CTA) scope: the expanding warps' writes reached shared memory before
+        // their own arrivals, and a cluster-scope release drains the SM's memory pipeline, about a
+        // microsecond a stage.
         Ring st;
-        for (int t = first; t < p.tiles; t += pairs) {
-            bool ok = true;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += pairs)
             for (int i = 0; i < steps && ok; ++i) {
                 ok = mbar_wait(&expd[st.slot], st.phase);
                 if (ok) mbar_arrive_cluster(ready_l + 8 * st.slot);
-                st.advance(stages);
+                st.advance(kStages);
             }
-            if (!ok) break;
-        }
-    } else if (warp == 1 && leader) {
+    } else if (warp == kWarpMma && leader) {
         // ---------------------------------------------------------------- MMA issue
         // The warp stays converged and one elected lane issues: with the loop in one lane's branch
         // the same instructions took 10 to 15 % longer (the descriptors are uniform registers, which
-        // divergent code has to move there one lane at a time).
-        const int n0 = p.bn < 256 ? p.bn : 256, n1 = p.bn - n0;
-        const uint32_t major = BACKWARD ? kIdescBMnMajor : 0u;
-        const uint32_t idesc0 = umma_idesc_bf16(2 * kRows, n0) | major, idesc1 = umma_idesc_bf16(2 * kRows, n1) | major;
+        // divergent code has to move there one lane at a time).  Between two stages' MMAs this warp
+        // executes some dozens of instructions, and the tensor pipe idles for as long as they take:
+        // no busy warp shares its scheduler.
+        const bool issuer = elect_one();
+        const uint32_t idesc = umma_idesc_bf16(2 * kRows, p.bn) | (BACKWARD ? kIdescBMnMajor : 0u);
+        const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sa));
+        const uint64_t b_desc0 = BACKWARD ? desc_mn_sw128(smem_u32(sb)) : umma_desc_sw128(smem_u32(sb));
+        const int a_hop = kABytes >> 4, b_hop = p.b_bytes >> 4;
+        // K = 16 further on, in descriptor units; the second 64 k of a K-major tile are its second half
+        constexpr int kBHop = (BACKWARD ? 2048 : 32) >> 4;
+        const int b_half = BACKWARD ? 4 * kBHop : p.b_bytes >> 5;
         Ring st, acc;
         int done = 0;
         bool ok = true;
         for (int t = first; t < p.tiles && ok; t += pairs, ++done) {
             // the accumulator's previous tile has been read
-            if (done >= nacc && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
+            if (done >= 2 && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
             tc_fence_after();
             const uint32_t d = tmem + acc.slot * 256;
             for (int i = 0; i < steps; ++i) {
-                if (!mbar_wait_spin(&ready[st.slot], st.phase)) ok = false;
-                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                const uint32_t a0 = smem_u32(sa + st.slot * kABytes), b0 = smem_u32(sb + st.slot * p.b_bytes);
-                if (elect_one()) {
+                if (!mbar_wait_spin(&ready[st.slot], st.phase)) { ok = false; break; }
+                if (issuer) {
+                    const uint64_t ad = a_desc0 + st.slot * a_hop, bd = b_desc0 + st.slot * b_hop;
 #pragma unroll
-                    for (int kk = 0; kk < kStep / 16; ++kk) {
-                        const uint64_t ad = umma_desc_sw128(a0 + 32 * kk);
-                        const uint64_t bd = BACKWARD ? desc_mn_sw128(b0 + 2048 * kk) : umma_desc_sw128(b0 + 32 * kk);
-                        umma_bf16_pair(d, ad, bd, idesc0, i > 0 || kk > 0);
-                        if (BACKWARD && n1)      // the outputs behind this CTA's first 128: the third group of 64
-                            umma_bf16_pair(d + 256, ad, desc_mn_sw128(b0 + 16384 + 2048 * kk), idesc1, i > 0 || kk > 0);
-                    }
-                    umma_commit_pair(&empty[st.slot], 3);
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16_pair(d, ad + (kk >> 2) * (kABytes >> 5) + 2 * (kk & 3), bd + (kk >> 2) * b_half + kBHop * (kk & 3),
+                                       idesc, kk > 0 || i > 0);
+                    umma_commit_pair(&empty[st.slot], pair_mask);
                 }
-                st.advance(stages);
+                st.advance(kStages);
             }
-            if (ok && elect_one()) umma_commit_pair(&acc_full[acc.slot], 3);
-            acc.advance(nacc);
+            if (ok && issuer) umma_commit_pair(&acc_full[acc.slot], pair_mask);
+            acc.advance(2);
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 8 && (warp & 3) != 1) {
         // ---------------------------------------------------------------- codes to BF16
-        // Four teams of two warps, each every fourth stage: expanding one stage is a chain of waits,
-        // loads, conversions, stores and a fence that takes longer than the stage's MMAs, so four
-        // stages are under way at once.
-        const int team = (warp - 8) >> 1, id = threadIdx.x & 63;
-        // Task q of a thread: block of 32 codes (row r, block b) of the codes tile.  Forward: rows of
-        // neighbouring lanes, both blocks of a row; backward: the blocks of a row side by side.
-        const int rows = BACKWARD ? kStep : half, blks = BACKWARD ? half / 32 : 2;
-        const uint32_t sw0 = smem_u32(sw), sb0 = smem_u32(sb);
-        constexpr int kMaxTasks = BACKWARD ? kMaxBN / 64 : 4;
-        uint32_t src[kMaxTasks], dst[kMaxTasks];
-        int trow[kMaxTasks], tblk[kMaxTasks];
-#pragma unroll
-        for (int q = 0; q < kMaxTasks; ++q) {
-            int r, b;
-            if constexpr (BACKWARD) {
-                r = (id + 64 * q) / blks;
-                b = (id + 64 * q) - r * blks;
-            } else {
-                r = id + 64 * (q >> 1);
-                b = q & 1;
-            }
-            trow[q] = r < rows ? r : -1;
-            tblk[q] = b;
-            // forward: chunk 2 (i % 4) + b of a 128-byte row, i % 4 the team
-            src[q] = sw0 + (BACKWARD ? r * p.w_pitch + ((b ^ ((r >> p.w_swz_shift) & p.w_swz_mask)) << 4)
-                                     : r * 128 + (((2 * team + b) ^ (r & 7)) << 4));
-            // forward: 64 k of an output, block b the half b; backward: 64 outputs of a row n, group b / 2
-            dst[q] = sb0 + (BACKWARD ? (b >> 1) * 8192 + r * 128 : r * 128) + ((((b & 1) * 4) ^ (r & 7)) << 4);
-        }
+        // Three teams of four warps, one a stage of the ring: expanding one stage is a chain of waits,
+        // loads, conversions, stores and a fence, so three stages are under way at once.  The warps on the
+        // issuing warp's scheduler (warp % 4 == 1) take no part.
+        const int index = (warp - 8) / 4 * 3 + (warp & 3) - ((warp & 3) > 1);    // 0 .. 11
+        const int team = index >> 2, id = (index & 3) * 32 + lane;
+        // A thread expands the blocks of 32 codes of one row of the codes tile, an output's four
+        // (forward) or a stored row's half / 32 (backward).  Neighbouring lanes have neighbouring rows,
+        // whose 16-byte chunks the swizzles of both tiles spread over the banks.
+        const int blks = BACKWARD ? half / 32 : 4;
+        const bool live = BACKWARD || id < half;
+        const uint32_t swz = (id >> p.w_swz_shift) & p.w_swz_mask;
+        const uint32_t src = smem_u32(sw) + team * p.w_bytes + id * p.w_pitch;
+        const uint32_t dst = smem_u32(sb) + team * p.b_bytes + id * 128 + ((id & 7) << 4);
+        const uint32_t dst_hop = BACKWARD ? kGroupBytes : p.b_bytes / 2;   // two blocks further on
+        const int stored = BACKWARD ? p.C : p.o.J;             // rows of W
+        const uint8_t *ws_end = p.ws + static_cast<long long>(stored) * p.ks;
+        uint32_t phase = 0;
+        bool filled = false, ok = true;
+        int i = team;                                          // this team's next stage of the tile
         pdl_wait();
-        constexpr int kSpan = kWSpan<BACKWARD>;
-        const int slots = p.w_slots;
-        const int copies = (steps + kSpan - 1) / kSpan;        // of a tile
-        long long base = 0, wbase = 0;                         // stages and copies of the tiles before
-        bool ok = true;
-        for (int t = first; t < p.tiles && ok; t += pairs, base += steps, wbase += copies) {
+        for (int t = first; t < p.tiles && ok; t += pairs, i -= steps) {
             const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
-            const int i0 = team;                               // this team's stages: team, team + 4, ...
-            long long f = base + i0;
-            int slot = static_cast<int>(f % stages);
-            uint32_t phase = static_cast<uint32_t>(f / stages) & 1u;
-            const long long wf = wbase + i0 / kSpan;
-            int cslot = static_cast<int>(wf % slots);
-            uint32_t cphase = static_cast<uint32_t>(wf / slots) & 1u;
-            uint32_t cur[kMaxTasks], nxt[BACKWARD ? kMaxTasks : 1];
-            uint4 words[BACKWARD ? 1 : kMaxTasks / 2];
-            if constexpr (BACKWARD) {
+            // row and first block of the scale bytes of stage i
+            const auto row = [&](int i) { return BACKWARD ? (step0 + i) * kStep + id : j0 + id; };
+            const auto blk = [&](int i) { return BACKWARD ? j0 / 32 : 4 * (step0 + i); };
+            uint2 next = load_scales(p.ws, ws_end, live && row(i) < stored, row(i), blk(i), blks, p.ks);
+            for (; i < steps; i += kTeams) {
+                const uint32_t e = scales_of(next, row(i), blk(i), p.ks);
+                next = load_scales(p.ws, ws_end, live && row(i + kTeams) < stored, row(i + kTeams), blk(i + kTeams), blks, p.ks);
+                if (!mbar_wait(&w_full[team], phase)) { ok = false; break; }
+                uint4 c[4];
 #pragma unroll
-                for (int q = 0; q < kMaxTasks; ++q) nxt[q] = scale_by_column(p, i0 * kStep + trow[q], j0 / 32 + tblk[q], trow[q] >= 0);
-            } else {
+                for (int b = 0; b < 4; ++b)
+                    if (live && b < blks) c[b] = lds128(src + ((b ^ swz) << 4));
+                if (filled && !mbar_wait(&empty[team], phase ^ 1u)) { ok = false; break; }
 #pragma unroll
-                for (int q = 0; q < kMaxTasks; q += 2) words[q / 2] = scale_words(p, j0 + trow[q], i0, trow[q] >= 0);
-            }
-            for (int i = i0, it = 0; i < steps; i += 4, ++it, f += 4) {
-                if constexpr (BACKWARD) {
-#pragma unroll
-                    for (int q = 0; q < kMaxTasks; ++q) {
-                        cur[q] = nxt[q];
-                        nxt[q] = scale_by_column(p, (i + 4) * kStep + trow[q], j0 / 32 + tblk[q], trow[q] >= 0);
-                    }
-                } else {
-                    // four scale bytes of a row: this stage's two and the next one's of this team
-#pragma unroll
-                    for (int q = 0; q < kMaxTasks; q += 2) {
-                        if (it & 1) {
-                            cur[q] >>= 16;
-                        } else {
-                            cur[q] = scale_bytes(p, words[q / 2], team);
-                            words[q / 2] = scale_words(p, j0 + trow[q], i + 8, trow[q] >= 0);
-                        }
-                    }
-                }
-                if (!mbar_wait(&w_full[cslot], cphase)) { ok = false; break; }
-                uint4 c[kMaxTasks];
-#pragma unroll
-                for (int q = 0; q < kMaxTasks; ++q)
-                    if (trow[q] >= 0) c[q] = lds128(src[q] + cslot * p.w_bytes);
-                if (f >= stages && !mbar_wait(&empty[slot], phase ^ 1u)) { ok = false; break; }
-                const uint32_t to = slot * p.b_bytes;
-#pragma unroll
-                for (int q = 0; q < kMaxTasks; ++q) {
-                    if (trow[q] >= 0) {
-                        const Factor fac = factor_of(BACKWARD ? cur[q] : (cur[q & ~1] >> (8 * (q & 1))) & 255u);
-                        const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
-#pragma unroll
-                        for (int jj = 0; jj < 4; ++jj) {
-                            uint32_t r[4];
-                            expand8(w[jj], fac, r);
-                            sts128((to + dst[q]) ^ (jj << 4), make_uint4(r[0], r[1], r[2], r[3]));
-                        }
-                    }
-                }
+                for (int b = 0; b < 4; ++b)
+                    if (live && b < blks) expand_block(c[b], (dst + (b >> 1) * dst_hop) ^ ((b & 1) << 6), (e >> (8 * b)) & 255u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&w_empty[cslot]);
-                    if (leader) mbar_arrive(&ready[slot]);
-                    else mbar_arrive(&expd[slot]);
+                    mbar_arrive(&w_empty[team]);
+                    if (leader) mbar_arrive(&ready[team]);
+                    else mbar_arrive(&expd[team]);
                 }
-                slot += 4;
-                if (slot >= stages) {
-                    slot -= stages;
-                    phase ^= 1u;
-                }
-                cslot += 4 / kSpan;
-                if (cslot >= slots) {
-                    cslot -= slots;
-                    cphase ^= 1u;
-                }
-            }
-            // a tile's last copy holds codes of up to four stages: the teams without one release it too
-            if (kSpan > 1 && ok && steps % kSpan != 0 && team >= steps % kSpan) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[cslot]);
+                phase ^= 1u;
+                filled = true;
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // ---------------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -544,30 +500,77 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const long long m = static_cast<long long>(t % p.tiles_m) * 2 * kRows + rank * kRows + quarter * 32 + lane;
             const int j0 = t / p.tiles_m * p.bn;
             if (!mbar_wait(&acc_full[acc.slot], acc.phase)) break;
+            if (p.splits > 1) break;            // one tile; its sums join below
             tc_fence_after();
             for (int c = 0; c < p.bn; c += 32) {
                 __syncwarp();                   // the loads are collective
-                uint32_t r[32];
-                tmem_ld32(tmem + lanes + acc.slot * 256 + c, r);
-                tmem_ld_wait_regs(r);
-                int j = j0 + c;                 // columns in order, but for the second MMA's
-                if (BACKWARD && p.bn > 256) {
-                    const int w = half - 128, cc = c - 256;
-                    j = j0 + (c < 256 ? (c / 128) * half + c % 128 : cc / w * half + 128 + cc % w);
-                }
-                if (m < p.o.M && j < p.o.J) write_columns(p.o, m, j, r);
+                uint32_t v[32];
+                tmem_ld32(tmem + lanes + acc.slot * 256 + c, v);
+                tmem_ld_wait_regs(v);
+                const int j = j0 + c;
+                if (m < p.o.M && j < p.o.J) write_columns(p.o, m, j, v);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc.slot);
-            acc.advance(nacc);
+            acc.advance(2);
+        }
+    }
+
+    if (p.splits > 1) {
+        // Partial sums of a tile: 32 columns belong to split (column / 32) % S.  Every warp takes part
+        // (six for each quarter of the rows); the others' columns go to their split's shared memory as
+        // [source][own columns / 32][4 columns][row] x 16 bytes, idle once the cluster's main loops are
+        // over, and are added in split order.
+        const int S = p.splits, quarter = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, row = quarter * 32 + lane;
+        const int chunks = p.bn / 32, own = (chunks + S - 1) / S;
+        __syncwarp();
+        tc_fence_before();
+        cluster_sync_all();
+        tc_fence_after();
+        for (int c = warp >> 2; c < chunks; c += kThreads / 128) {
+            const int to = c % S;
+            if (to == split) continue;
+            uint32_t v[32];
+            tmem_ld32(tmem + lanes + 32 * c, v);
+            tmem_ld_wait_regs(v);
+            const uint32_t base = dsmem_addr(smem_u32(smem), 2 * to + rank) + ((split * own + c / S) * 8 * kRows + row) * 16;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) st_dsmem_v4(base + q * kRows * 16, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+        }
+        cluster_sync_all();
+        const long long m = static_cast<long long>(first % p.tiles_m) * 2 * kRows + rank * kRows + row;
+        const int j0 = first / p.tiles_m * p.bn;
+        for (int c = split + S * (warp >> 2); c < chunks; c += S * (kThreads / 128)) {
+            __syncwarp();
+            uint32_t v[32];
+            tmem_ld32(tmem + lanes + 32 * c, v);
+            tmem_ld_wait_regs(v);
+            float sum[32];
+            for (int s = 0; s < S; ++s) {
+                const uint32_t from = smem_u32(smem) + ((s * own + c / S) * 8 * kRows + row) * 16;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint4 o = s == split ? make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3])
+                                               : lds128(from + q * kRows * 16);
+                    sum[4 * q] = (s ? sum[4 * q] : 0.f) + __uint_as_float(o.x);
+                    sum[4 * q + 1] = (s ? sum[4 * q + 1] : 0.f) + __uint_as_float(o.y);
+                    sum[4 * q + 2] = (s ? sum[4 * q + 2] : 0.f) + __uint_as_float(o.z);
+                    sum[4 * q + 3] = (s ? sum[4 * q + 3] : 0.f) + __uint_as_float(o.w);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(sum[q]);
+            const int j = j0 + c * 32;
+            if (m < p.o.M && j < p.o.J) write_columns(p.o, m, j, v);
         }
     }
 
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, kTmemCols);
     }

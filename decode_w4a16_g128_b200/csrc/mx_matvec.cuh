@@ -31,18 +31,18 @@ struct Params {
     int gated;
 };
 
-// Codes j and j + 4 of every word -> BF16 pairs times the factor.
-__device__ __forceinline__ void expand_pairs(uint32_t v, const mxg::Factor &s, uint32_t (&r)[4]) {
+// Codes j and j + 4 of a word -> BF16 pairs times the factor (`more`: a second one, 0 for none).
+__device__ __forceinline__ void expand_pairs(uint32_t v, uint32_t f, uint32_t more, uint32_t (&r)[4]) {
     const uint32_t u = v >> 8;
     r[0] = (v & 0x000F000Fu) * 0x1040u;
     r[1] = (v & 0x00F000F0u) * 0x0104u;
     r[2] = (u & 0x000F000Fu) * 0x1040u;
     r[3] = (u & 0x00F000F0u) * 0x0104u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i] & 0x81C081C0u, s.f);
-    if (s.more) {
+    for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i] & 0x81C081C0u, f);
+    if (more) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i], s.more);
+        for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i], more);
     }
 }
 
@@ -95,11 +95,14 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
 
 template <int RB, int NB>
 __device__ __forceinline__ void multiply(const Codes<RB> &st, const Rows<NB> &x, float (&acc)[RB][NB][2][4]) {
-    mxg::Factor f[RB][2];
+    uint32_t f[RB][2], more[RB][2];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) f[rb][h] = mxg::factor_of(st.e[rb][h]);
+        for (int h = 0; h < 2; ++h) {
+            f[rb][h] = mxg::factor_of(min(st.e[rb][h], mxg::kOneFactor));
+            more[rb][h] = st.e[rb][h] > mxg::kOneFactor ? mxg::second_factor_of(st.e[rb][h]) : 0u;
+        }
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         uint32_t b[NB][4];
@@ -114,8 +117,8 @@ __device__ __forceinline__ void multiply(const Codes<RB> &st, const Rows<NB> &x,
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
             uint32_t lo[4], hi[4];
-            expand_pairs(word_of(st.c[rb][0], w), f[rb][0], lo);
-            expand_pairs(word_of(st.c[rb][1], w), f[rb][1], hi);
+            expand_pairs(word_of(st.c[rb][0], w), f[rb][0], more[rb][0], lo);
+            expand_pairs(word_of(st.c[rb][1], w), f[rb][1], more[rb][1], hi);
             const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t r[32];
                 tmem_ld32(tmem + lanes + acc.slot * kAccCols + c, r);
                 tmem_ld_wait_regs(r);
-                if (m < p.o.M && j0 + c < p.o.J) mxg::write_columns(p.o, m, j0 + c, r);
+                if (m < p.o.M && j0 + c < p.o.J) mxg::write_columns<mxg::kPlain>(p.o, m, j0 + c, r);
             }
             tc_fence_before();
             __syncwarp();

@@ -37,6 +37,14 @@ int mx_sizes(int64_t M, int64_t N, int64_t K) {
     return W4A16_OK;
 }
 
+using MxGemm = void(const CUtensorMap, const CUtensorMap, const mxg::Params);
+MxGemm *mx_gemm_of(bool backward, int epilogue) {
+    if (backward) return mxg::gemm_kernel<true, mxg::kPlain>;
+    if (epilogue == mxg::kGated) return mxg::gemm_kernel<false, mxg::kGated>;
+    if (epilogue == mxg::kGatedBackward) return mxg::gemm_kernel<false, mxg::kGatedBackward>;
+    return mxg::gemm_kernel<false, mxg::kPlain>;
+}
+
 cudaLaunchAttribute mx_cluster(int ctas) {
     cudaLaunchAttribute a;
     a.id = cudaLaunchAttributeClusterDimension;
@@ -51,9 +59,11 @@ int mx_device(DeviceInfo **d) {
     int rc = current_device(&dev);
     if (!rc) rc = device_setup(dev, d);
     if (rc || (*d)->mx_ready) return rc;
-    cudaError_t e = cudaFuncSetAttribute(mxg::gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(mxg::gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
+    cudaError_t e = cudaSuccess;
+    for (MxGemm *kernel : {mx_gemm_of(false, mxg::kPlain), mx_gemm_of(false, mxg::kGated),
+                           mx_gemm_of(false, mxg::kGatedBackward), mx_gemm_of(true, mxg::kPlain)})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mx4::a4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mx4::kSmemBytes);
     for (int S = 1; S <= mxg::kMaxSplits && e == cudaSuccess; S *= 2) {
@@ -64,7 +74,7 @@ int mx_device(DeviceInfo **d) {
         cudaLaunchAttribute cl = mx_cluster(2 * S);
         cfg.attrs = &cl;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[S], mxg::gemm_kernel<true>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[S], mx_gemm_of(true, mxg::kPlain), &cfg);
     }
     if (e != cudaSuccess) return cuda_fail(e);
     (*d)->mx_ready = true;
@@ -101,7 +111,6 @@ mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilo
     o.dh = static_cast<const uint16_t *>(dh);
     o.M = static_cast<int>(M);
     o.J = static_cast<int>(J);
-    o.epilogue = epilogue;
     const int64_t row = epilogue == mxg::kGated ? J / 2 : J;
     o.wide = row % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     return o;
@@ -178,8 +187,7 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     if (rc) return rc;
     const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, d->mx_clusters[1]);
     const dim3 grid(static_cast<unsigned>(2 * p.splits * clusters), 1, 1);
-    const auto kernel = backward ? mxg::gemm_kernel<true> : mxg::gemm_kernel<false>;
-    return mx_launch(kernel, grid, 2 * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
+    return mx_launch(mx_gemm_of(backward, epilogue), grid, 2 * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
 }
 
 // Outputs of a CTA pair of the 4-bit product: the fewest column-rounds of the persistent grid; an MMA

@@ -17,8 +17,8 @@
 // mx_entry.cuh).  Where the tiles leave SMs idle, S pairs share a tile (a cluster of 2 S CTAs), each a
 // run of the stages; their partial sums meet in shared memory over the cluster, added in split order.
 //
-// Roles (768 threads): warp 1 MMA issue (leader) and tensor memory, warps 4-7 epilogue, twelve of warps
-// 8-23 expand codes in three teams, and beside warp 1 on its scheduler one warp that copies codes, one
+// Roles (768 threads): warp 1 MMA issue (leader) and tensor memory, warps 0, 2-7 and 21 epilogue,
+// twelve of warps 8-23 expand codes in three teams, and beside warp 1 on its scheduler one warp that copies codes, one
 // that copies x, and the peer's that forwards "expanded" to the leader.  The ring has three stages, one
 // a team.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's four expanding warps, the peer's
 // forwarder), empty[s] (both CTAs; the stage's MMAs completed), exp[s] (peer: its four expanding
@@ -39,11 +39,11 @@ constexpr int kRows = 128;               // x rows of a CTA
 constexpr int kStep = 128;               // contraction of a stage
 constexpr int kStages = 3;
 constexpr int kABytes = kRows * kStep * 2;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;
 constexpr int kTeams = kStages, kTeamWarps = 4;   // expanding warps, see there
 constexpr int kMaxSplits = 4;
 // Warps with w % 4 == 1 share the issuing warp's scheduler: light roles.
-constexpr int kWarpMma = 1, kWarpCodes = 9, kWarpX = 13, kWarpForward = 17;
+constexpr int kWarpMma = 1, kWarpCodes = 9, kWarpX = 13, kWarpForward = 17, kWarpEpi = 21;
 constexpr int kTmemCols = 512;
 constexpr int kMaxBN = 256;              // outputs of a pair
 constexpr int kBarBytes = 256;
@@ -150,14 +150,13 @@ struct Output {
     uint16_t *out;
     const uint16_t *dh;       // bf16 [M, J/2] (kGatedBackward)
     int M, J;
-    int epilogue;
     int wide;                 // 32-byte stores: rows and base are multiples of 32 bytes
 };
 
-// 32 accumulator columns of one row: outputs j .. j + 31 (j a multiple of 32 or, at the start of a
-// second MMA's columns, still of 32).
+// 32 accumulator columns of one row: outputs j .. j + 31, j a multiple of 32.
+template <int EPILOGUE>
 __device__ __forceinline__ void write_columns(const Output &p, long long m, int j, const uint32_t (&r)[32]) {
-    if (p.epilogue == kPlain) {
+    if constexpr (EPILOGUE == kPlain) {
         uint16_t *dst = p.out + m * p.J + j;
         if ((p.J & 7) == 0) {
 #pragma unroll
@@ -173,11 +172,8 @@ __device__ __forceinline__ void write_columns(const Output &p, long long m, int 
             for (int i = 0; i < 32; ++i)
                 if (j + i < p.J) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[i])));
         }
-        return;
-    }
-    // J is a multiple of 16: 8 gate columns and their 8 up columns
-    const long long h = m * (p.J / 2) + j / 2;
-    if (p.epilogue == kGated) {
+    } else if constexpr (EPILOGUE == kGated) {    // J is a multiple of 16: 8 gate columns and their 8 up columns
+        uint16_t *dst = p.out + m * (p.J / 2) + j / 2;
         uint4 o[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -187,21 +183,22 @@ __device__ __forceinline__ void write_columns(const Output &p, long long m, int 
                 a[i] = mx::gated(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]));
             o[q] = pack8(a);
         }
-        if (j + 16 < p.J) store_pair(p.out + h, o[0], o[1], p.wide);
-        else *reinterpret_cast<uint4 *>(p.out + h) = o[0];
-        return;
-    }
+        if (j + 16 < p.J) store_pair(dst, o[0], o[1], p.wide);
+        else *reinterpret_cast<uint4 *>(dst) = o[0];
+    } else {
+        const uint16_t *src = p.dh + m * (p.J / 2) + j / 2;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        if (j + 16 * q >= p.J) break;
-        const uint4 d = ldg_v4(p.dh + h + 8 * q);
-        const float dh[8] = {bf16_lo_to_f32(d.x), bf16_hi_to_f32(d.x), bf16_lo_to_f32(d.y), bf16_hi_to_f32(d.y),
-                             bf16_lo_to_f32(d.z), bf16_hi_to_f32(d.z), bf16_lo_to_f32(d.w), bf16_hi_to_f32(d.w)};
-        float a[8], b[8];
+        for (int q = 0; q < 2; ++q) {
+            if (j + 16 * q >= p.J) break;
+            const uint4 d = ldg_v4(src + 8 * q);
+            const float dh[8] = {bf16_lo_to_f32(d.x), bf16_hi_to_f32(d.x), bf16_lo_to_f32(d.y), bf16_hi_to_f32(d.y),
+                                 bf16_lo_to_f32(d.z), bf16_hi_to_f32(d.z), bf16_lo_to_f32(d.w), bf16_hi_to_f32(d.w)};
+            float a[8], b[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            mx::gated_backward(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]), dh[i], a[i], b[i]);
-        store_pair(p.out + m * p.J + j + 16 * q, pack8(a), pack8(b), p.wide);
+            for (int i = 0; i < 8; ++i)
+                mx::gated_backward(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]), dh[i], a[i], b[i]);
+            store_pair(p.out + m * p.J + j + 16 * q, pack8(a), pack8(b), p.wide);
+        }
     }
 }
 
@@ -295,7 +292,7 @@ __device__ __forceinline__ void st_dsmem_v4(uint32_t cluster_addr, uint4 v) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <bool BACKWARD>
+template <bool BACKWARD, int EPILOGUE>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -344,6 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ready_l = dsmem_addr(smem_u32(ready), lead), acc_empty_l = dsmem_addr(smem_u32(acc_empty), lead);
     const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
 
+    // two epilogue warps for every quarter of the lanes, 32 columns in turn
+    const bool epilogue = (warp < 8 && warp != kWarpMma) || warp == kWarpEpi;
+    const int epi_set = warp >= 4 && warp < 8;
     if (warp == kWarpX && lane == 0) {
         // ---------------------------------------------------------------- x by TMA
         prefetch_tmap(&tm_x);
@@ -446,15 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // issuing warp's scheduler (warp % 4 == 1) take no part.
         const int index = (warp - 8) / 4 * 3 + (warp & 3) - ((warp & 3) > 1);    // 0 .. 11
         const int team = index >> 2, id = (index & 3) * 32 + lane;
-        // A thread expands the blocks of 32 codes of one row of the codes tile, an output's four
-        // (forward) or a stored row's half / 32 (backward).  Neighbouring lanes have neighbouring rows,
-        // whose 16-byte chunks the swizzles of both tiles spread over the banks.
+        // A thread expands blocks of 32 codes of one row of the codes tile, an output's four (forward)
+        // or a stored row's half / 32 (backward); forward tiles of 32 or 64 rows a CTA have four or two
+        // threads a row, with every fourth or second block each.  Neighbouring lanes have neighbouring
+        // rows, whose 16-byte chunks the swizzles of both tiles spread over the banks.
         const int blks = BACKWARD ? half / 32 : 4;
-        const bool live = BACKWARD || id < half;
-        const uint32_t swz = (id >> p.w_swz_shift) & p.w_swz_mask;
-        const uint32_t src = smem_u32(sw) + team * p.w_bytes + id * p.w_pitch;
-        const uint32_t dst = smem_u32(sb) + team * p.b_bytes + id * 128 + ((id & 7) << 4);
-        const uint32_t dst_hop = BACKWARD ? kGroupBytes : p.b_bytes / 2;   // two blocks further on
+        const int share = BACKWARD ? 1 : (half == 32 ? 4 : (half == 64 ? 2 : 1));
+        const int r = share > 1 ? id & (half - 1) : id, b0 = share > 1 ? id / half : 0;
+        const bool live = BACKWARD || r < half;
+        const uint32_t swz = (r >> p.w_swz_shift) & p.w_swz_mask;
+        uint32_t src[4], dst[4];                               // of block b0 + q share; src = 0: none
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int b = b0 + q * share;
+            src[q] = live && b < blks ? smem_u32(sw) + team * p.w_bytes + r * p.w_pitch + ((b ^ swz) << 4) : 0u;
+            dst[q] = smem_u32(sb) + team * p.b_bytes + (b >> 1) * (BACKWARD ? kGroupBytes : p.b_bytes / 2) + r * 128 +
+                     ((((b & 1) * 4) ^ (r & 7)) << 4);
+        }
         const int stored = BACKWARD ? p.C : p.o.J;             // rows of W
         const uint8_t *ws_end = p.ws + static_cast<long long>(stored) * p.ks;
         uint32_t phase = 0;
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = first; t < p.tiles && ok; t += pairs, i -= steps) {
             const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
             // row and first block of the scale bytes of stage i
-            const auto row = [&](int i) { return BACKWARD ? (step0 + i) * kStep + id : j0 + id; };
+            const auto row = [&](int i) { return BACKWARD ? (step0 + i) * kStep + r : j0 + r; };
             const auto blk = [&](int i) { return BACKWARD ? j0 / 32 : 4 * (step0 + i); };
             uint2 next = load_scales(p.ws, ws_end, live && row(i) < stored, row(i), blk(i), blks, p.ks);
             for (; i < steps; i += kTeams) {
@@ -473,12 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(&w_full[team], phase)) { ok = false; break; }
                 uint4 c[4];
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (live && b < blks) c[b] = lds128(src + ((b ^ swz) << 4));
+                for (int q = 0; q < 4; ++q)
+                    if (src[q]) c[q] = lds128(src[q]);
                 if (filled && !mbar_wait(&empty[team], phase ^ 1u)) { ok = false; break; }
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (live && b < blks) expand_block(c[b], (dst + (b >> 1) * dst_hop) ^ ((b & 1) << 6), (e >> (8 * b)) & 255u);
+                for (int q = 0; q < 4; ++q)
+                    if (src[q]) expand_block(c[q], dst[q], (e >> (8 * (b0 + q * share))) & 255u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -490,41 +498,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 filled = true;
             }
         }
-    } else if (warp >= 4 && warp < 8) {
-        // ---------------------------------------------------------------- epilogue
-        const int quarter = warp & 3;
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        pdl_wait();
-        Ring acc;
-        for (int t = first; t < p.tiles; t += pairs) {
-            const long long m = static_cast<long long>(t % p.tiles_m) * 2 * kRows + rank * kRows + quarter * 32 + lane;
-            const int j0 = t / p.tiles_m * p.bn;
-            if (!mbar_wait(&acc_full[acc.slot], acc.phase)) break;
-            if (p.splits > 1) break;            // one tile; its sums join below
-            tc_fence_after();
-            for (int c = 0; c < p.bn; c += 32) {
-                __syncwarp();                   // the loads are collective
-                uint32_t v[32];
-                tmem_ld32(tmem + lanes + acc.slot * 256 + c, v);
-                tmem_ld_wait_regs(v);
-                const int j = j0 + c;
-                if (m < p.o.M && j < p.o.J) write_columns(p.o, m, j, v);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc.slot);
-            acc.advance(2);
-        }
+    } else if (epilogue && p.splits > 1) {
+        mbar_wait(&acc_full[0], 0);
     }
 
-    if (p.splits > 1) {
+    const int quarter = warp & 3, chunks = p.bn / 32, S = p.splits, own = (chunks + S - 1) / S;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, row = quarter * 32 + lane;
+    if (S > 1) {
         // Partial sums of a tile: 32 columns belong to split (column / 32) % S.  Every warp takes part
         // (six for each quarter of the rows); the others' columns go to their split's shared memory as
         // [source][own columns / 32][4 columns][row] x 16 bytes, idle once the cluster's main loops are
-        // over, and are added in split order.
-        const int S = p.splits, quarter = warp & 3;
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, row = quarter * 32 + lane;
-        const int chunks = p.bn / 32, own = (chunks + S - 1) / S;
+        // over.
         __syncwarp();
         tc_fence_before();
         cluster_sync_all();
@@ -540,30 +524,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 8; ++q) st_dsmem_v4(base + q * kRows * 16, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
         }
         cluster_sync_all();
-        const long long m = static_cast<long long>(first % p.tiles_m) * 2 * kRows + rank * kRows + row;
-        const int j0 = first / p.tiles_m * p.bn;
-        for (int c = split + S * (warp >> 2); c < chunks; c += S * (kThreads / 128)) {
-            __syncwarp();
-            uint32_t v[32];
-            tmem_ld32(tmem + lanes + 32 * c, v);
-            tmem_ld_wait_regs(v);
-            float sum[32];
-            for (int s = 0; s < S; ++s) {
-                const uint32_t from = smem_u32(smem) + ((s * own + c / S) * 8 * kRows + row) * 16;
+    }
+    if (epilogue) {
+        // ---------------------------------------------------------------- epilogue
+        pdl_wait();
+        Ring acc;
+        for (int t = first; t < p.tiles; t += pairs) {
+            const long long m = static_cast<long long>(t % p.tiles_m) * 2 * kRows + rank * kRows + row;
+            const int j0 = t / p.tiles_m * p.bn;
+            if (S == 1 && !mbar_wait(&acc_full[acc.slot], acc.phase)) break;
+            tc_fence_after();
+            for (int c = split + S * epi_set; c < chunks; c += 2 * S) {
+                __syncwarp();                   // the loads are collective
+                uint32_t v[32];
+                tmem_ld32(tmem + lanes + acc.slot * 256 + 32 * c, v);
+                tmem_ld_wait_regs(v);
+                for (int s = 0; s < S; ++s) {   // the other splits' sums, in their order
+                    if (s == split) continue;
+                    const uint32_t from = smem_u32(smem) + ((s * own + c / S) * 8 * kRows + row) * 16;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint4 o = s == split ? make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3])
-                                               : lds128(from + q * kRows * 16);
-                    sum[4 * q] = (s ? sum[4 * q] : 0.f) + __uint_as_float(o.x);
-                    sum[4 * q + 1] = (s ? sum[4 * q + 1] : 0.f) + __uint_as_float(o.y);
-                    sum[4 * q + 2] = (s ? sum[4 * q + 2] : 0.f) + __uint_as_float(o.z);
-                    sum[4 * q + 3] = (s ? sum[4 * q + 3] : 0.f) + __uint_as_float(o.w);
+                    for (int q = 0; q < 8; ++q) {
+                        const uint4 o = lds128(from + q * kRows * 16);
+                        v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + __uint_as_float(o.x));
+                        v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + __uint_as_float(o.y));
+                        v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + __uint_as_float(o.z));
+                        v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + __uint_as_float(o.w));
+                    }
                 }
+                const int j = j0 + 32 * c;
+                if (m < p.o.M && j < p.o.J) write_columns<EPILOGUE>(p.o, m, j, v);
             }
-#pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(sum[q]);
-            const int j = j0 + c * 32;
-            if (m < p.o.M && j < p.o.J) write_columns(p.o, m, j, v);
+            if (S > 1) break;                   // one tile a cluster
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc.slot);
+            acc.advance(2);
         }
     }
 

@@ -114,9 +114,11 @@ def sigmoid(g):
         return 1.0 / (1.0 + np.exp(-g))
 
 
-# FP32 evaluation of the scalar formulas: expf (2 ulp), and at most a dozen more operations, each
-# off by 2^-24 of its result; none but 1 + g (1 - s) subtracts, and that one is bounded by its terms.
-SCALAR = 16 * 2.0 ** -24
+# FP32 evaluation of the scalar formulas: the exponential's documented bound is 2 + 1.173 |g| steps of
+# 2^-23, the division's 2, and at most a dozen more operations are off by 2^-24 of their result each;
+# none but 1 + g (1 - s) subtracts, and that one is bounded by its terms.
+def scalar(g):
+    return (2 + 1.173 * np.abs(g) + 2) * 2.0 ** -23 + 12 * 2.0 ** -24
 
 
 def gate_up(x, w):
@@ -124,7 +126,7 @@ def gate_up(x, w):
     gu, s = x @ w.T, sum_error(x, w)
     (g, u), (eg, eu) = split(gu, 1), split(s, 1)
     h = g * sigmoid(g) * u
-    e = 1.1 * (np.abs(u) + eu) * eg + np.abs(g * sigmoid(g)) * eu + SCALAR * np.abs(h)
+    e = 1.1 * (np.abs(u) + eu) * eg + np.abs(g * sigmoid(g)) * eu + scalar(g) * np.abs(h)
     return h, HALF_STEP * (np.abs(h) + e) + e + TINY
 
 
@@ -136,8 +138,8 @@ def gate_up_backward(x, w, dh):
     dg, du = dh * u * s * (1 + g * (1 - s)), dh * g * s
     a = np.abs(dh)
     # s (1 + g (1 - s)): its terms' magnitudes bound the cancellation; 1 - s loses 2^-24 absolutely
-    edg = a * (0.5 * (np.abs(u) + eu) * eg + 1.1 * eu) + SCALAR * a * np.abs(u) * s * (1 + 2 * np.abs(g))
-    edu = a * 1.1 * eg + SCALAR * np.abs(du)
+    edg = a * (0.5 * (np.abs(u) + eu) * eg + 1.1 * eu) + scalar(g) * a * np.abs(u) * s * (1 + 2 * np.abs(g))
+    edu = a * 1.1 * eg + scalar(g) * np.abs(du)
     d = np.stack([dg.reshape(len(x), -1, 8), du.reshape(len(x), -1, 8)], 2).reshape(len(x), -1)
     e = np.stack([edg.reshape(len(x), -1, 8), edu.reshape(len(x), -1, 8)], 2).reshape(len(x), -1)
     return d, HALF_STEP * (np.abs(d) + e) + e + TINY

@@ -185,7 +185,7 @@ def test_gate_up_is_the_two_layers():
     g, u = x @ ref.values(gq, gs).T, x @ ref.values(uq, us).T
     h = g * ref.sigmoid(g) * u
     got = host(w4.w4a16_mx_gate_up(dev_bf16(x), *dev(wq, s)))
-    near(got, h, (ref.HALF_STEP + 2 * ref.SCALAR) * np.abs(h) + ref.TINY)
+    near(got, h, (ref.HALF_STEP + 2 * ref.scalar(g)) * np.abs(h) + ref.TINY)
     t = w4.interleave_gate_up(dev(gq, gs)[0], dev(uq, us)[0])
     assert np.array_equal(t.cpu().numpy().view(np.uint32), wq)
 

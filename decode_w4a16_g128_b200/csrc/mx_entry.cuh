@@ -231,13 +231,17 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
     return mx_launch(mx4::a4_kernel, grid, 2, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, p);
 }
 
-// Few rows of x: forward products alone.
-bool mx_few_rows(int64_t M) { return M <= mxv::kMaxM; }
+// Few rows of x take the matvec: up to 16 always, up to 32 where the weight is small.  Measured, us,
+// matvec / GEMM: M = 16 N x K 9728 x 2560 11.5 / 19.9, 2560 x 9728 15.6 / 20.1; M = 32 1024 x 2560
+// 6.8 / 10.7, 4096 x 2560 9.0 / 12.3, but 2560 x 9728 26.7 / 20.1 and 19456 x 2560 38 / 26.5.
+bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
+    return M <= 16 || (M <= mxv::kMaxM && N * K <= (int64_t(1) << 24));
+}
 
-template <int RB, int NB, int WARPS, int D>
+template <int RB, int NB, int WARPS, int D, int CTAS>
 int mx_matvec_launch(const mxv::Params &p, void *stream) {
     const dim3 grid(static_cast<unsigned>((int64_t(p.N) + 16 * RB - 1) / (16 * RB)), 1, 1);
-    return mx_launch(mxv::matvec_kernel<RB, NB, WARPS, D>, grid, 1, 32 * WARPS, 0, stream, p);
+    return mx_launch(mxv::matvec_kernel<RB, NB, WARPS, D, CTAS>, grid, 1, 32 * WARPS, 0, stream, p);
 }
 
 int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *ws, void *out, int64_t M, int64_t N,
@@ -251,10 +255,20 @@ int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *w
     p.N = static_cast<int>(N);
     p.K = static_cast<int>(K);
     p.gated = gated ? 1 : 0;
-    (void)d;
-    if (M <= 8) return mx_matvec_launch<1, 1, 8, 3>(p, stream);
-    if (M <= 16) return mx_matvec_launch<1, 2, 8, 3>(p, stream);
-    return mx_matvec_launch<1, 4, 8, 2>(p, stream);
+    // Warps of a CTA (they share its rows' K): as many as leave every CTA resident at once, 16 (one
+    // CTA an SM), 8 (two) or 4 (five).  Measured at M = 1, us, with 16 / 8 / 4 warps: N x K 2560 x 9728
+    // 10.7 / 9.9 / 13.1, 4096 x 2560 5.8 / 4.0 / 5.4, 9728 x 2560 12.4 / 8.7 / 7.0.
+    const int64_t blocks = (N + 15) / 16;
+    if (M <= 8) {
+        if (blocks <= d->sms) return mx_matvec_launch<1, 1, 16, 2, 1>(p, stream);
+        if (blocks <= 2 * d->sms) return mx_matvec_launch<1, 1, 8, 2, 2>(p, stream);
+        return mx_matvec_launch<1, 1, 4, 2, 5>(p, stream);
+    }
+    if (M <= 16) {
+        if (blocks <= 2 * d->sms) return mx_matvec_launch<1, 2, 8, 2, 2>(p, stream);
+        return mx_matvec_launch<1, 2, 4, 1, 5>(p, stream);
+    }
+    return mx_matvec_launch<1, 4, 8, 1, 2>(p, stream);
 }
 
 unsigned stream_grid(int64_t words, int sms) {
@@ -320,7 +334,7 @@ int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, vo
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(y, s[0].bytes, stream);   // an empty sum
-    if (mx_few_rows(M)) return mx_matvec(d, x, wq, scales, y, M, N, K, false, stream);
+    if (mx_few_rows(M, N, K)) return mx_matvec(d, x, wq, scales, y, M, N, K, false, stream);
     return mx_gemm(d, x, wq, scales, nullptr, y, M, N, K, N, K, false, mxg::kPlain, stream);
 }
 
@@ -355,7 +369,7 @@ int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, v
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(h, s[0].bytes, stream);   // silu(0) 0 = +0
-    if (mx_few_rows(M)) return mx_matvec(d, x, wq, scales, h, M, 2 * N2, K, true, stream);
+    if (mx_few_rows(M, 2 * N2, K)) return mx_matvec(d, x, wq, scales, h, M, 2 * N2, K, true, stream);
     return mx_gemm(d, x, wq, scales, nullptr, h, M, 2 * N2, K, 2 * N2, K, false, mxg::kGated, stream);
 }
 

@@ -129,8 +129,8 @@ __device__ __forceinline__ void multiply(const Codes<RB> &st, const Rows<NB> &x,
     }
 }
 
-template <int RB, int NB, int WARPS, int D>
-__global__ void __launch_bounds__(32 * WARPS) matvec_kernel(const Params p) {
+template <int RB, int NB, int WARPS, int D, int CTAS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS) matvec_kernel(const Params p) {
     __shared__ float red[WARPS][RB][16][8 * NB + 1];
     pdl_launch_dependents();
     pdl_wait();

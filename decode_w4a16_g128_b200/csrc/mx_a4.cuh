@@ -17,8 +17,9 @@
 // five stages of the ring: a scale buffer is written again only after the barrier that says the stage's
 // MMAs are done.
 //
-// Roles (384 threads): warp 0 codes by TMA, warp 1 MMA issue (leader) and tensor memory, warps 2 and 3
-// scales of x and of W, warps 4-11 epilogue.
+// Roles (512 threads): warp 0 codes by TMA, warp 1 MMA issue (leader) and tensor memory, warps 2, 3, 12,
+// 14 and 15 scales (with two loader warps their instructions took longer than the MMAs), warps 4-11
+// epilogue; warp 13 would share the issuing warp's scheduler and stays idle.
 #pragma once
 
 #include "mx_gemm.cuh"
@@ -29,7 +30,8 @@ namespace mx4 {
 using mxg::elect_one;
 using mxg::Ring;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+constexpr int kLoaders = 5, kGroups = 10;  // loader warps; groups of 32 rows: four of x, six of W
 constexpr int kRows = 128;                // x rows of a CTA
 constexpr int kStep = 256;                // K of a stage
 constexpr int kStages = 5;
@@ -91,87 +93,69 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int m, int n, uint32_t id) {
 
 // ------------------------------------------------------------------ scale bytes
 
-// Bytes first .. first + 15 (blocks of K) of a stored row of ks scale bytes, 127 behind its end and
-// for rows outside.  One 16-byte load where rows are 16-byte aligned; else five aligned words, shifted
-// into place (the array starts on a 16-byte boundary; its last word may be cut off: read by bytes).
-__device__ __forceinline__ uint32_t word_inside(const uint8_t *at, const uint8_t *end) {
-    if (at + 4 <= end) return __ldg(reinterpret_cast<const uint32_t *>(at));
-    uint32_t v = 0;
-    for (int i = 0; i < 3; ++i)
-        if (at + i < end) v |= static_cast<uint32_t>(__ldg(at + i)) << (8 * i);
-    return v;
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ uint4 scale16(const uint8_t *s, int rows, int ks, int row, int first, bool aligned) {
-    const uint4 none = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if (row >= rows || first >= ks) return none;
-    const uint8_t *at = s + static_cast<long long>(row) * ks + first;
-    if (aligned) return ldg_nc_v4(at);
-    const uint8_t *end = s + static_cast<long long>(rows) * ks;
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 3u);
-    uint32_t w[5], v[4];
+
+// 16 bytes at a 16-byte boundary of an array of scale bytes; behind its end nothing is read.
+__device__ __forceinline__ uint4 scale_chunk(const uint8_t *at, const uint8_t *end) {
+    if (at + 16 <= end) return ldg_nc_v4(at);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    for (int i = 0; i < 16; ++i)
+        if (at + i < end) w[i >> 2] |= static_cast<uint32_t>(__ldg(at + i)) << (8 * (i & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Bytes off .. off + 15 of two neighbouring chunks, the first `valid` of them; 127 for the others.
+__device__ __forceinline__ uint4 scale_window(const uint4 &a, const uint4 &b, uint32_t off, int valid) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8) {
 #pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = word_inside(at - off + 4 * i, end);
-    const int valid = ks - first;
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
-        const int n = valid - 4 * i;                        // valid bytes of this word
-        const uint32_t mask = n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
-        v[i] = (v[i] & mask) | (0x7F7F7F7Fu & ~mask);
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(w[i], w[i + 1], 8 * (off & 3));
+    if (valid < 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = valid - 4 * i;
+            const uint32_t mask = n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+            v[i] = (v[i] & mask) | (0x7F7F7F7Fu & ~mask);
+        }
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// A loader warp's share of every tile: scales of `groups` x 32 rows from row0(t), two stages at a time.
-template <int GROUPS, typename Row0>
-__device__ __forceinline__ void load_scales(const uint8_t *s, int rows, int K, int first, int step_t, int tiles, int steps,
-                                            uint32_t dst0, uint64_t *empty, uint32_t ready_l, int lane, Row0 row0) {
-    const int ks = K / mx::kBlock;
-    const bool aligned = ks % 16 == 0;
-    Ring st;
-    long long issued = 0;
-    for (int t = first; t < tiles; t += step_t) {
-        const int r0 = row0(t) + lane;
-        uint4 v[GROUPS];
-#pragma unroll
-        for (int c = 0; c < GROUPS; ++c) v[c] = scale16(s, rows, ks, r0 + 32 * c, 0, aligned);
-        for (int i = 0; i < steps; i += 2) {
-            uint4 cur[GROUPS];
-#pragma unroll
-            for (int c = 0; c < GROUPS; ++c) cur[c] = v[c];
-#pragma unroll
-            for (int c = 0; c < GROUPS; ++c) v[c] = scale16(s, rows, ks, r0 + 32 * c, 8 * (i + 2), aligned);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (i + u >= steps) break;
-                if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) return;
-                ++issued;
-                const uint32_t dst = dst0 + st.slot * kSBytes + lane * 16;
-#pragma unroll
-                for (int kc = 0; kc < 2; ++kc)
-#pragma unroll
-                    for (int q = 0; q < (GROUPS + 3) / 4; ++q) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int g = 4 * q + c;
-                            if (g < GROUPS) {
-                                const uint4 &x = cur[g < GROUPS ? g : 0];
-                                w[c] = u == 0 ? (kc == 0 ? x.x : x.y) : (kc == 0 ? x.z : x.w);
-                            } else {
-                                w[c] = 0x7F7F7F7Fu;
-                            }
-                        }
-                        sts128(dst + (kc * 3 + q) * kChunkBytes, make_uint4(w[0], w[1], w[2], w[3]));
-                    }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(ready_l + 8 * st.slot);
-                st.advance(kStages);
-            }
-        }
+// A group of 32 rows, a row a lane: its sixteen bytes of two stages lie in one or two aligned chunks,
+// the second of which is the first of the next two stages: one 16-byte load a row for two stages
+// whatever the rows' alignment, issued two stages ahead.
+struct ScaleGroup {
+    const uint8_t *at;                          // the chunk of the row's first byte; null: no such row
+    const uint8_t *end;
+    uint32_t off;
+    uint4 a, b;
+    __device__ __forceinline__ void start(const uint8_t *s, int rows, int ks, int row) {
+        const long long byte = static_cast<long long>(row) * ks;
+        at = row < rows ? s + (byte & ~15ll) : nullptr;
+        end = s + static_cast<long long>(rows) * ks;
+        off = static_cast<uint32_t>(byte) & 15u;
+        a = at ? scale_chunk(at, end) : make_uint4(0u, 0u, 0u, 0u);
+        b = at ? scale_chunk(at + 16, end) : make_uint4(0u, 0u, 0u, 0u);
     }
-}
+    // the bytes of stages i and i + 1; the chunk for stages i + 2 and i + 3 is asked for
+    __device__ __forceinline__ uint4 next(int i, int ks, bool aligned) {
+        uint4 v = a;
+        if (!aligned || 8 * i + 16 > ks || !at) v = scale_window(a, b, off, at ? ks - 8 * i : 0);
+        a = b;
+        if (at && 8 * i + 32 < ks + 16) b = scale_chunk(at + 8 * i + 32, end);
+        return v;
+    }
+};
 
 // ------------------------------------------------------------------ the kernel
 
@@ -194,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         pdl_launch_dependents();
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&ready[i], 1 + 2 * 2);   // codes of both CTAs, two loader warps each
+            mbar_init(&ready[i], 1 + 2 * kLoaders);   // codes of both CTAs, the loader warps of each
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -241,52 +225,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (leader) {
             // ------------------------------------------------------------ MMA issue (converged warp)
+            const bool issuer = elect_one();
             const uint32_t id0 = idesc_mxf4(2 * kRows, p.bn, 0), id2 = idesc_mxf4(2 * kRows, p.bn, 2);
-            const int wgroups = p.bn > 128 ? 2 : 1;
+            const bool two_groups = p.bn > 128;
+            const uint64_t a_desc0 = umma_desc_sw128(smem_u32(smem)), b_desc0 = umma_desc_sw128(smem_u32(smem + kOffB));
+            const uint64_t s_desc0 = desc_scales(smem_u32(smem + kOffS));
             Ring st, acc;
             int done = 0;
             bool ok = true;
             for (int t = first; t < p.tiles && ok; t += pairs, ++done) {
-                if (done >= 2 && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) ok = false;
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                if (done >= 2 && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + acc.slot * kAccCols;
                 for (int i = 0; i < steps; ++i) {
-                    if (!mbar_wait_spin(&ready[st.slot], st.phase)) ok = false;
-                    if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-                    const uint32_t a0 = smem_u32(smem + st.slot * kABytes), b0 = smem_u32(smem + kOffB + st.slot * kBBytes);
-                    const uint32_t s0 = smem_u32(smem + kOffS + st.slot * kSBytes);
-                    const uint32_t sc = tmem + kScaleCol0 + st.slot * kScaleCols;   // x: 2 x 4 columns, W: 2 x 8
-                    if (elect_one()) {
+                    if (!mbar_wait_spin(&ready[st.slot], st.phase)) { ok = false; break; }
+                    if (issuer) {
+                        const uint64_t ad = a_desc0 + st.slot * (kABytes >> 4), bd = b_desc0 + st.slot * (kBBytes >> 4);
+                        const uint64_t sd = s_desc0 + st.slot * (kSBytes >> 4);
+                        const uint32_t sc = tmem + kScaleCol0 + st.slot * kScaleCols;   // x: 2 x 4 columns, W: 2 x 8
 #pragma unroll
                         for (int kc = 0; kc < 2; ++kc) {
-                            copy_scales_pair(sc + 4 * kc, desc_scales(s0 + kc * 3 * kChunkBytes));
-                            copy_scales_pair(sc + 8 + 8 * kc, desc_scales(s0 + (kc * 3 + 1) * kChunkBytes));
-                            if (wgroups > 1)
-                                copy_scales_pair(sc + 8 + 8 * kc + 4, desc_scales(s0 + (kc * 3 + 2) * kChunkBytes));
+                            const uint64_t from = sd + kc * (3 * kChunkBytes >> 4);
+                            copy_scales_pair(sc + 4 * kc, from);
+                            copy_scales_pair(sc + 8 + 8 * kc, from + (kChunkBytes >> 4));
+                            if (two_groups) copy_scales_pair(sc + 8 + 8 * kc + 4, from + 2 * (kChunkBytes >> 4));
                         }
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_mxf4_pair(d, umma_desc_sw128(a0 + 32 * kk), umma_desc_sw128(b0 + 32 * kk), kk & 1 ? id2 : id0,
-                                           sc + 4 * (kk >> 1), sc + 8 + 8 * (kk >> 1), i > 0 || kk > 0);
+                            umma_mxf4_pair(d, ad + 2 * kk, bd + 2 * kk, kk & 1 ? id2 : id0, sc + 4 * (kk >> 1),
+                                           sc + 8 + 8 * (kk >> 1), kk > 0 || i > 0);
                         umma_commit_pair(&empty[st.slot], 3);
                     }
                     st.advance(kStages);
                 }
-                if (ok && elect_one()) umma_commit_pair(&acc_full[acc.slot], 3);
+                if (ok && issuer) umma_commit_pair(&acc_full[acc.slot], 3);
                 acc.advance(2);
             }
         }
-    } else if (warp == 2) {
-        pdl_wait();
-        load_scales<4>(p.xs, p.o.M, p.K, first, pairs, p.tiles, steps, smem_u32(smem + kOffS), empty, ready_l, lane,
-                       [&](int t) { return (t % p.tiles_m) * 2 * kRows + static_cast<int>(rank) * kRows; });
-    } else if (warp == 3) {
-        pdl_wait();
-        const auto row0 = [&](int t) { return t / p.tiles_m * p.bn; };
-        const uint32_t dst = smem_u32(smem + kOffS) + kChunkBytes;
-        if (p.bn > 128) load_scales<6>(p.ws, p.o.J, p.K, first, pairs, p.tiles, steps, dst, empty, ready_l, lane, row0);
-        else load_scales<4>(p.ws, p.o.J, p.K, first, pairs, p.tiles, steps, dst, empty, ready_l, lane, row0);
+    } else if (warp < 4 || warp > 11) {
+        if (warp != 13) {
+            // ------------------------------------------------------------ scales: groups `index` and index + 5
+            const int index = warp < 4 ? warp - 2 : (warp == 12 ? 2 : warp - 11);
+            const int ks = p.K / mx::kBlock, wgroups = (p.bn + 31) / 32;
+            const bool aligned = ks % 16 == 0;
+            pdl_wait();
+            Ring st;
+            long long issued = 0;
+            bool ok = true;
+            for (int t = first; t < p.tiles && ok; t += pairs) {
+                const int row_x = (t % p.tiles_m) * 2 * kRows + static_cast<int>(rank) * kRows, row_w = t / p.tiles_m * p.bn;
+                ScaleGroup g[kGroups / kLoaders];
+#pragma unroll
+                for (int q = 0; q < kGroups / kLoaders; ++q) {
+                    const int n = index + q * kLoaders;
+                    if (n < 4) g[q].start(p.xs, p.o.M, ks, row_x + 32 * n + lane);
+                    else g[q].start(p.ws, n - 4 < wgroups ? p.o.J : 0, ks, row_w + 32 * (n - 4) + lane);
+                }
+                for (int i = 0; i < steps && ok; i += 2) {
+                    uint4 v[kGroups / kLoaders];
+#pragma unroll
+                    for (int q = 0; q < kGroups / kLoaders; ++q) v[q] = g[q].next(i, ks, aligned);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (i + u >= steps) break;
+                        if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
+                        ++issued;
+#pragma unroll
+                        for (int q = 0; q < kGroups / kLoaders; ++q) {
+                            // row 32 c + lane of 128: word c of 16 bytes `lane`
+                            const int n = index + q * kLoaders, c = n < 4 ? n : n - 4;
+                            const uint32_t dst = smem_u32(smem + kOffS) + st.slot * kSBytes +
+                                                 (n < 4 ? 0 : (c < 4 ? kChunkBytes : 2 * kChunkBytes)) + lane * 16 + (c & 3) * 4;
+                            sts32(dst, u == 0 ? v[q].x : v[q].z);
+                            sts32(dst + 3 * kChunkBytes, u == 0 ? v[q].y : v[q].w);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(ready_l + 8 * st.slot);
+                        st.advance(kStages);
+                    }
+                }
+            }
+        }
     } else {
         // ---------------------------------------------------------------- epilogue: half of the columns a warp
         const int quarter = warp & 3, c0 = (warp - 4) / 4 * half;

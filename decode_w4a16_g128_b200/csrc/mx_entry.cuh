@@ -199,7 +199,7 @@ int mx_a4_width(int64_t M, int64_t N, int pairs) {
     for (int bn = 64; bn <= mx4::kMaxBN; bn += 64) {
         const int64_t tiles = tm * ((N + bn - 1) / bn), rounds = (tiles + pairs - 1) / pairs;
         const int64_t c = rounds * std::max(bn, 100);
-        if (!best || c < cost) {
+        if (!best || c <= cost) {
             best = bn;
             cost = c;
         }

@@ -9,13 +9,13 @@
 // every 128 rows and K = 128, 32 lanes x 4 columns (row 32 c + l in lane l, column c; its four bytes
 // are four blocks, an MMA takes two of them), the same in all four lane quarters; each CTA needs those
 // of its own rows of x and of all BN outputs.  Loader warps gather them from the stored rows [rows, K/32],
-// 16 bytes a row for two stages, put them into that order in shared memory, and the issuing thread
-// copies them with tcgen05.cp just before the stage's MMAs.
+// 32 bytes a row for four stages (a barrier's wait and arrival a stage took them longer than the MMAs),
+// put them into that order in shared memory, and the issuing thread copies them with tcgen05.cp just
+// before a stage's MMAs.
 //
 // Tensor memory: two accumulators of 192 columns (a tile's epilogue runs under the next one's main
-// loop, which at K = 2560 takes only about 4000 cycles) and a scale buffer of 24 columns for each of the
-// five stages of the ring: a scale buffer is written again only after the barrier that says the stage's
-// MMAs are done.
+// loop, which at K = 2560 takes only about 4000 cycles) and a scale buffer of 24 columns for each stage of
+// the ring: a scale buffer is written again only after the barrier that says the stage's MMAs are done.
 //
 // Roles (512 threads): warp 0 codes by TMA, warp 1 MMA issue (leader) and tensor memory, warps 2, 3, 12,
 // 14 and 15 scales (with two loader warps their instructions took longer than the MMAs), warps 4-11
@@ -40,19 +40,23 @@ constexpr int kABytes = kRows * kStep / 2;
 constexpr int kBBytes = kMaxBN / 2 * kStep / 2;
 constexpr int kChunkBytes = 512;          // scales of 128 rows, K = 128
 constexpr int kSBytes = 2 * 3 * kChunkBytes;   // of a stage: [K half][x, W rows 0-127, W rows 128-255]
+constexpr int kSpan = 4, kSpans = 2;      // stages of a scale slot, slots
 constexpr int kAccCols = 192, kScaleCol0 = 2 * kAccCols, kScaleCols = 24;
 constexpr int kTmemCols = 512;
 static_assert(kScaleCol0 + kStages * kScaleCols <= kTmemCols, "tensor memory budget");
 constexpr int kEpiWarps = 8;
-constexpr int kOffB = kStages * kABytes, kOffS = kOffB + kStages * kBBytes, kOffBar = kOffS + kStages * kSBytes;
-constexpr int kSmemBytes = kOffBar + 256 + 1024;   // + barriers, alignment slack
+// Shared memory: stages of A, of B, scale slots, barriers, staging of ragged rows, alignment slack.
+// (Keeping all of K of a CTA's rows of x there while it streams W alone was no faster.)
+constexpr int kOffB = kStages * kABytes, kOffS = kOffB + kStages * kBBytes, kOffBar = kOffS + kSpans * kSpan * kSBytes;
+constexpr int kBarBytes = 256, kOffStage = kOffBar + kBarBytes;
+constexpr int kSmemBytes = kOffStage + kEpiWarps * mxg::kStageBytes + 1024;
 static_assert(kBBytes % 1024 == 0 && kSmemBytes <= 227 * 1024, "shared memory layout");
 
 struct Params {
     mxg::Output o;            // M rows, J = N outputs
     const uint8_t *xs, *ws;   // scales [M, K/32], [N, K/32]
     int K, bn;
-    int tiles_m, tiles;
+    int tiles_n, tiles;
 };
 
 // ------------------------------------------------------------------ PTX
@@ -97,9 +101,8 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// 16 bytes at a 16-byte boundary of an array of scale bytes; behind its end nothing is read.
+// 16 bytes of an array of scale bytes; behind its end nothing is read.
 __device__ __forceinline__ uint4 scale_chunk(const uint8_t *at, const uint8_t *end) {
-    if (at + 16 <= end) return ldg_nc_v4(at);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     for (int i = 0; i < 16; ++i)
         if (at + i < end) w[i >> 2] |= static_cast<uint32_t>(__ldg(at + i)) << (8 * (i & 3));
@@ -131,29 +134,46 @@ __device__ __forceinline__ uint4 scale_window(const uint4 &a, const uint4 &b, ui
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// A group of 32 rows, a row a lane: its sixteen bytes of two stages lie in one or two aligned chunks,
-// the second of which is the first of the next two stages: one 16-byte load a row for two stages
-// whatever the rows' alignment, issued two stages ahead.
-struct ScaleGroup {
-    const uint8_t *at;                          // the chunk of the row's first byte; null: no such row
-    const uint8_t *end;
+// A predicated 16-byte load into registers that hold something else if it is not made: no branch, after
+// which the compiler would move the loaded value, and wait for it there.
+__device__ __forceinline__ void load_chunk_if(bool p, const uint8_t *at, uint4 &v) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(at), "r"(p ? 1u : 0u));
+}
+
+// A row's 32 scale bytes of a span, as the two or three aligned chunks that hold them.
+struct ScaleItem {
+    uint4 a, b, c;
+    const uint8_t *at;                          // of chunk a
     uint32_t off;
-    uint4 a, b;
-    __device__ __forceinline__ void start(const uint8_t *s, int rows, int ks, int row) {
-        const long long byte = static_cast<long long>(row) * ks;
-        at = row < rows ? s + (byte & ~15ll) : nullptr;
-        end = s + static_cast<long long>(rows) * ks;
+    int valid;                                  // bytes inside the row
+    __device__ __forceinline__ void fetch(const uint8_t *s, const uint8_t *end, bool live, int ks, int row, int first,
+                                          bool aligned) {
+        const long long byte = live ? static_cast<long long>(row) * ks + first : 0;
+        valid = live ? ks - first : 0;
+        at = s + (byte & ~15ll);
         off = static_cast<uint32_t>(byte) & 15u;
-        a = at ? scale_chunk(at, end) : make_uint4(0u, 0u, 0u, 0u);
-        b = at ? scale_chunk(at + 16, end) : make_uint4(0u, 0u, 0u, 0u);
+        const int need = valid > 0 ? valid + static_cast<int>(off) : 0;
+        a = b = c = make_uint4(0u, 0u, 0u, 0u);
+        load_chunk_if(need > 0 && at + 16 <= end, at, a);
+        load_chunk_if(need > 16 && at + 32 <= end, at + 16, b);
+        if (!aligned) load_chunk_if(need > 32 && at + 48 <= end, at + 32, c);
     }
-    // the bytes of stages i and i + 1; the chunk for stages i + 2 and i + 3 is asked for
-    __device__ __forceinline__ uint4 next(int i, int ks, bool aligned) {
-        uint4 v = a;
-        if (!aligned || 8 * i + 16 > ks || !at) v = scale_window(a, b, off, at ? ks - 8 * i : 0);
-        a = b;
-        if (at && 8 * i + 32 < ks + 16) b = scale_chunk(at + 8 * i + 32, end);
-        return v;
+    // The array's last, incomplete chunk was not loaded: its bytes one by one.
+    __device__ __forceinline__ void complete(const uint8_t *end) {
+        if (valid <= 0 || at + 48 <= end) return;
+        if (at + 16 > end) a = scale_chunk(at, end);
+        if (at + 32 > end) b = scale_chunk(at + 16, end);
+        c = scale_chunk(at + 32, end);
+    }
+    __device__ __forceinline__ uint4 window(int half, bool aligned) const {
+        const uint4 &lo = half ? b : a, &hi = half ? c : b;
+        if (aligned && valid >= 32) return lo;
+        return scale_window(lo, hi, off, valid - 16 * half);
     }
 };
 
@@ -163,23 +183,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     a4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sb = smem + kOffB, *ss = smem + kOffS;
     uint64_t *ready = reinterpret_cast<uint64_t *>(smem + kOffBar);
-    uint64_t *empty = ready + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 2;
+    uint64_t *empty = ready + kStages, *s_full = empty + kStages, *s_empty = s_full + kSpans;
+    uint64_t *acc_full = s_empty + kSpans, *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
-    static_assert((2 * kStages + 4) * 8 + 4 <= 256, "barrier area");
+    static_assert(kSpan == 4, "two turns of the issue loop");
+    static_assert((2 * kStages + 2 * kSpans + 4) * 8 + 4 <= kBarBytes, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int steps = (p.K + kStep - 1) / kStep;
     const int half = p.bn / 2;
-    const int pairs = static_cast<int>(gridDim.x) / 2, first = static_cast<int>(blockIdx.x) / 2;
+    // tiles of this pair, neighbours along the outputs: tile t has rows t / tiles_n
+    const long long pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int t0 = static_cast<int>(pair * p.tiles / pairs), t1 = static_cast<int>((pair + 1) * p.tiles / pairs);
+    const auto row_of = [&](int t) { return t / p.tiles_n * 2 * kRows + static_cast<int>(rank) * kRows; };
+    const auto out_of = [&](int t) { return t % p.tiles_n * p.bn; };
 
     if (threadIdx.x == 0) {
         pdl_launch_dependents();
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&ready[i], 1 + 2 * kLoaders);   // codes of both CTAs, the loader warps of each
+            mbar_init(&ready[i], 1);           // codes of both CTAs
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kSpans; ++i) {
+            mbar_init(&s_full[i], 2 * kLoaders);   // the loader warps of both CTAs
+            mbar_init(&s_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -196,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t ready_l = dsmem_addr(smem_u32(ready), 0), acc_empty_l = dsmem_addr(smem_u32(acc_empty), 0);
+    const uint32_t s_full_l = dsmem_addr(smem_u32(s_full), 0);
 
     if (warp == 0) {
         if (lane == 0) {
@@ -206,14 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring st;
             long long issued = 0;
             bool ok = true;
-            for (int t = first; t < p.tiles && ok; t += pairs) {
-                const int row = (t % p.tiles_m) * 2 * kRows + static_cast<int>(rank) * kRows;
-                const int out = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
+            for (int t = t0; t < t1 && ok; ++t) {
+                const int row = row_of(t), out = out_of(t) + static_cast<int>(rank) * half;
                 for (int i = 0; i < steps; ++i) {
                     if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
                     if (leader) mbar_arrive_expect_tx(&ready[st.slot], 2 * (kABytes + half * (kStep / 2)));
                     tma_load_2d_pair(smem + st.slot * kABytes, &tm_x, ready_l + 8 * st.slot, i * (kStep / 8), row);
-                    tma_load_2d_pair(smem + kOffB + st.slot * kBBytes, &tm_w, ready_l + 8 * st.slot, i * (kStep / 8), out);
+                    tma_load_2d_pair(sb + st.slot * kBBytes, &tm_w, ready_l + 8 * st.slot, i * (kStep / 8), out);
                     ++issued;
                     st.advance(kStages);
                 }
@@ -228,35 +259,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool issuer = elect_one();
             const uint32_t id0 = idesc_mxf4(2 * kRows, p.bn, 0), id2 = idesc_mxf4(2 * kRows, p.bn, 2);
             const bool two_groups = p.bn > 128;
-            const uint64_t a_desc0 = umma_desc_sw128(smem_u32(smem)), b_desc0 = umma_desc_sw128(smem_u32(smem + kOffB));
-            const uint64_t s_desc0 = desc_scales(smem_u32(smem + kOffS));
-            Ring st, acc;
+            const uint64_t a_desc0 = umma_desc_sw128(smem_u32(smem)), b_desc0 = umma_desc_sw128(smem_u32(sb));
+            const uint64_t s_desc0 = desc_scales(smem_u32(ss));
+            // Two stages a turn: what surrounds a stage's MMAs, waits foremost, takes this warp nearly as long
+            // as the MMAs take the tensor cores.
+            const auto issue = [&](uint32_t d, int slot, int scale_stage, bool first) {
+                const uint64_t ad = a_desc0 + slot * (kABytes >> 4), bd = b_desc0 + slot * (kBBytes >> 4);
+                const uint64_t sd = s_desc0 + scale_stage * (kSBytes >> 4);
+                const uint32_t sc = tmem + kScaleCol0 + slot * kScaleCols;   // x: 2 x 4 columns, W: 2 x 8
+#pragma unroll
+                for (int kc = 0; kc < 2; ++kc) {
+                    const uint64_t from = sd + kc * (3 * kChunkBytes >> 4);
+                    copy_scales_pair(sc + 4 * kc, from);
+                    copy_scales_pair(sc + 8 + 8 * kc, from + (kChunkBytes >> 4));
+                    if (two_groups) copy_scales_pair(sc + 8 + 8 * kc + 4, from + 2 * (kChunkBytes >> 4));
+                }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_mxf4_pair(d, ad + 2 * kk, bd + 2 * kk, kk & 1 ? id2 : id0, sc + 4 * (kk >> 1), sc + 8 + 8 * (kk >> 1),
+                                   kk > 0 || !first);
+                umma_commit_pair(&empty[slot], 3);
+            };
+            Ring st, sp, acc;
             int done = 0;
             bool ok = true;
-            for (int t = first; t < p.tiles && ok; t += pairs, ++done) {
+            for (int t = t0; t < t1 && ok; ++t, ++done) {
                 if (done >= 2 && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + acc.slot * kAccCols;
-                for (int i = 0; i < steps; ++i) {
-                    if (!mbar_wait_spin(&ready[st.slot], st.phase)) { ok = false; break; }
-                    if (issuer) {
-                        const uint64_t ad = a_desc0 + st.slot * (kABytes >> 4), bd = b_desc0 + st.slot * (kBBytes >> 4);
-                        const uint64_t sd = s_desc0 + st.slot * (kSBytes >> 4);
-                        const uint32_t sc = tmem + kScaleCol0 + st.slot * kScaleCols;   // x: 2 x 4 columns, W: 2 x 8
-#pragma unroll
-                        for (int kc = 0; kc < 2; ++kc) {
-                            const uint64_t from = sd + kc * (3 * kChunkBytes >> 4);
-                            copy_scales_pair(sc + 4 * kc, from);
-                            copy_scales_pair(sc + 8 + 8 * kc, from + (kChunkBytes >> 4));
-                            if (two_groups) copy_scales_pair(sc + 8 + 8 * kc + 4, from + 2 * (kChunkBytes >> 4));
-                        }
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_mxf4_pair(d, ad + 2 * kk, bd + 2 * kk, kk & 1 ? id2 : id0, sc + 4 * (kk >> 1),
-                                           sc + 8 + 8 * (kk >> 1), kk > 0 || i > 0);
-                        umma_commit_pair(&empty[st.slot], 3);
+                for (int i = 0; i < steps; i += 2) {
+                    const bool two = i + 1 < steps, last = (i & 2) || i + 2 >= steps;      // of its scale slot
+                    Ring st1 = st;
+                    st1.advance(kStages);
+                    if (!(i & 2) && !mbar_wait_spin(&s_full[sp.slot], sp.phase)) { ok = false; break; }
+                    const bool now0 = mbar_test_wait(&ready[st.slot], st.phase), now1 = !two || mbar_test_wait(&ready[st1.slot], st1.phase);
+                    if (!now0 && !mbar_wait_spin(&ready[st.slot], st.phase)) { ok = false; break; }
+                    if (issuer) issue(d, st.slot, sp.slot * kSpan + (i & 2), i == 0);
+                    if (two) {
+                        if (!now1 && !mbar_wait_spin(&ready[st1.slot], st1.phase)) { ok = false; break; }
+                        if (issuer) issue(d, st1.slot, sp.slot * kSpan + (i & 2) + 1, false);
+                        st1.advance(kStages);
                     }
-                    st.advance(kStages);
+                    st = st1;
+                    if (last) {
+                        if (issuer) umma_commit_pair(&s_empty[sp.slot], 3);
+                        sp.advance(kSpans);
+                    }
                 }
                 if (ok && issuer) umma_commit_pair(&acc_full[acc.slot], 3);
                 acc.advance(2);
@@ -264,46 +312,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 4 || warp > 11) {
         if (warp != 13) {
-            // ------------------------------------------------------------ scales: groups `index` and index + 5
+            // ------------------------------------------------------------ scales
+            // This warp's groups of 32 rows, a row a lane: `index` and index + 5.  An item is a span of
+            // four stages of a tile; items are fetched two ahead, over the tiles' borders too.
             const int index = warp < 4 ? warp - 2 : (warp == 12 ? 2 : warp - 11);
-            const int ks = p.K / mx::kBlock, wgroups = (p.bn + 31) / 32;
+            const int ks = p.K / mx::kBlock, wgroups = (p.bn + 31) / 32, spans = (steps + kSpan - 1) / kSpan;
             const bool aligned = ks % 16 == 0;
-            pdl_wait();
-            Ring st;
-            long long issued = 0;
-            bool ok = true;
-            for (int t = first; t < p.tiles && ok; t += pairs) {
-                const int row_x = (t % p.tiles_m) * 2 * kRows + static_cast<int>(rank) * kRows, row_w = t / p.tiles_m * p.bn;
-                ScaleGroup g[kGroups / kLoaders];
+            constexpr int kOf = kGroups / kLoaders;
+            const uint8_t *xs_end = p.xs + static_cast<long long>(p.o.M) * ks, *ws_end = p.ws + static_cast<long long>(p.o.J) * ks;
+            const auto fetch = [&](ScaleItem(&v)[kOf], int t, int span) {
+                if (t >= t1) return;
 #pragma unroll
-                for (int q = 0; q < kGroups / kLoaders; ++q) {
+                for (int q = 0; q < kOf; ++q) {
                     const int n = index + q * kLoaders;
-                    if (n < 4) g[q].start(p.xs, p.o.M, ks, row_x + 32 * n + lane);
-                    else g[q].start(p.ws, n - 4 < wgroups ? p.o.J : 0, ks, row_w + 32 * (n - 4) + lane);
+                    const int row = n < 4 ? row_of(t) + 32 * n + lane : out_of(t) + 32 * (n - 4) + lane;
+                    v[q].fetch(n < 4 ? p.xs : p.ws, n < 4 ? xs_end : ws_end, n < 4 ? row < p.o.M : n - 4 < wgroups && row < p.o.J, ks,
+                               row, 32 * span, aligned);
                 }
-                for (int i = 0; i < steps && ok; i += 2) {
-                    uint4 v[kGroups / kLoaders];
+            };
+            const auto put = [&](ScaleItem(&v)[kOf], int slot) {
 #pragma unroll
-                    for (int q = 0; q < kGroups / kLoaders; ++q) v[q] = g[q].next(i, ks, aligned);
+                for (int q = 0; q < kOf; ++q) {
+                    v[q].complete(index + q * kLoaders < 4 ? xs_end : ws_end);
+                    // row 32 c + lane of 128: word c of 16 bytes `lane`
+                    const int n = index + q * kLoaders, c = n < 4 ? n : n - 4;
+                    const uint32_t dst = smem_u32(ss) + slot * kSpan * kSBytes +
+                                         (n < 4 ? 0 : (c < 4 ? kChunkBytes : 2 * kChunkBytes)) + lane * 16 + (c & 3) * 4;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (i + u >= steps) break;
-                        if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
-                        ++issued;
-#pragma unroll
-                        for (int q = 0; q < kGroups / kLoaders; ++q) {
-                            // row 32 c + lane of 128: word c of 16 bytes `lane`
-                            const int n = index + q * kLoaders, c = n < 4 ? n : n - 4;
-                            const uint32_t dst = smem_u32(smem + kOffS) + st.slot * kSBytes +
-                                                 (n < 4 ? 0 : (c < 4 ? kChunkBytes : 2 * kChunkBytes)) + lane * 16 + (c & 3) * 4;
-                            sts32(dst, u == 0 ? v[q].x : v[q].z);
-                            sts32(dst + 3 * kChunkBytes, u == 0 ? v[q].y : v[q].w);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(ready_l + 8 * st.slot);
-                        st.advance(kStages);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 w = v[q].window(h, aligned);      // stages 2 h and 2 h + 1
+                        sts32(dst + 2 * h * kSBytes, w.x);
+                        sts32(dst + 2 * h * kSBytes + 3 * kChunkBytes, w.y);
+                        sts32(dst + (2 * h + 1) * kSBytes, w.z);
+                        sts32(dst + (2 * h + 1) * kSBytes + 3 * kChunkBytes, w.w);
                     }
+                }
+            };
+            pdl_wait();
+            ScaleItem item[2][kOf];
+            int t = t0, span = 0;                       // of the item to fetch next
+            const auto step = [&]() {
+                if (++span == spans) {
+                    span = 0;
+                    ++t;
+                }
+            };
+            fetch(item[0], t, span);
+            step();
+            fetch(item[1], t, span);
+            step();
+            Ring sp;
+            const long long items = static_cast<long long>(t1 - t0) * spans;
+            bool ok = true;
+            for (long long n = 0; n < items && ok; n += 2) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (n + u >= items) break;
+                    if (n + u >= kSpans && !mbar_wait(&s_empty[sp.slot], sp.phase ^ 1u)) { ok = false; break; }
+                    put(item[u], sp.slot);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(s_full_l + 8 * sp.slot);
+                    sp.advance(kSpans);
+                    fetch(item[u], t, span);
+                    step();
                 }
             }
         }
@@ -313,9 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         pdl_wait();
         Ring acc;
-        for (int t = first; t < p.tiles; t += pairs) {
-            const long long m = static_cast<long long>(t % p.tiles_m) * 2 * kRows + rank * kRows + quarter * 32 + lane;
-            const int j0 = t / p.tiles_m * p.bn;
+        const uint32_t stage = smem_u32(smem + kOffStage) + (warp - 4) * mxg::kStageBytes;
+        for (int t = t0; t < t1; ++t) {
+            const long long m = static_cast<long long>(row_of(t)) + quarter * 32 + lane;
+            const int j0 = out_of(t);
             if (!mbar_wait(&acc_full[acc.slot], acc.phase)) break;
             tc_fence_after();
             for (int c = c0; c < c0 + half; c += 32) {
@@ -323,7 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t r[32];
                 tmem_ld32(tmem + lanes + acc.slot * kAccCols + c, r);
                 tmem_ld_wait_regs(r);
-                if (m < p.o.M && j0 + c < p.o.J) mxg::write_columns<mxg::kPlain>(p.o, m, j0 + c, r);
+                const int j = j0 + c;
+                if (j >= p.o.J) break;
+                if (p.o.J & 7) mxg::write_ragged(p.o, m - lane, j, r, stage, lane);
+                else if (m < p.o.M) mxg::write_columns<mxg::kPlain>(p.o, m, j, r);
             }
             tc_fence_before();
             __syncwarp();

@@ -123,11 +123,11 @@ mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilo
 struct MxShape {
     int bn = 0, splits = 1;
 };
-MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, const DeviceInfo *d) {
+MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragged, const DeviceInfo *d) {
     const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows), steps = (C + mxg::kStep - 1) / mxg::kStep;
     MxShape best;
     int64_t cost = 0;
-    for (int bn = 64; bn <= mxg::kMaxBN; bn += backward ? 64 : 32) {
+    for (int bn = 64; bn <= (ragged ? mxg::kMaxRaggedBN : mxg::kMaxBN); bn += backward ? 64 : 32) {
         const int64_t tiles = tm * ((J + bn - 1) / bn);
         const int64_t mma = 8 * std::max(bn / 2, 52) + 60, stage = std::max<int64_t>(mma, 400 + bn);
         for (int S = 1; S <= mxg::kMaxSplits; S *= 2) {
@@ -148,7 +148,8 @@ MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, const Devi
 // D = A . W^T (forward) or A . W (backward) on the tensor cores: A bf16 [M, C], J outputs.
 int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws, const void *dh, void *out, int64_t M,
             int64_t J, int64_t C, int64_t N, int64_t K, bool backward, int epilogue, void *stream) {
-    const MxShape shape = mx_gemm_shape(M, J, C, backward, d);
+    const bool ragged = epilogue == mxg::kPlain && J % 8 != 0;
+    const MxShape shape = mx_gemm_shape(M, J, C, backward, ragged, d);
     mxg::Params p;
     p.o = mx_output(out, dh, M, J, epilogue);
     p.ws = ws;
@@ -177,7 +178,7 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
         p.w_swz_shift = 1;
         p.w_swz_mask = 3;
     }
-    const int smem = mxg::smem_bytes(p.b_bytes, p.w_bytes);
+    const int smem = mxg::smem_bytes(p.b_bytes, p.w_bytes, ragged);
 
     CUtensorMap tx, tw;
     int rc = encode_2d(d, &tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a, C, M, C * 2, 64, mxg::kRows, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -218,7 +219,7 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
     p.bn = mx_a4_width(M, N, pairs);
     const int64_t tm = (M + 2 * mx4::kRows - 1) / (2 * mx4::kRows), tiles = tm * ((N + p.bn - 1) / p.bn);
     if (tiles >= kSizeLimit) return W4A16_ERR_UNSUPPORTED;
-    p.tiles_m = static_cast<int>(tm);
+    p.tiles_n = static_cast<int>((N + p.bn - 1) / p.bn);
     p.tiles = static_cast<int>(tiles);
     CUtensorMap tx, tw;
     int rc = encode_2d(d, &tx, CU_TENSOR_MAP_DATA_TYPE_UINT32, xq, K / 8, M, K / 2, mx4::kStep / 8, mx4::kRows,

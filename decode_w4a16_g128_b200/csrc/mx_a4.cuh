@@ -48,8 +48,10 @@ constexpr int kEpiWarps = 8;
 // Shared memory: stages of A, of B, scale slots, barriers, staging of ragged rows, alignment slack.
 // (Keeping all of K of a CTA's rows of x there while it streams W alone was no faster.)
 constexpr int kOffB = kStages * kABytes, kOffS = kOffB + kStages * kBBytes, kOffBar = kOffS + kSpans * kSpan * kSBytes;
-constexpr int kBarBytes = 256, kOffStage = kOffBar + kBarBytes;
-constexpr int kSmemBytes = kOffStage + kEpiWarps * mxg::kStageBytes + 1024;
+constexpr int kBarBytes = 1024, kOffStage = kOffBar + kBarBytes;
+constexpr int kStageBytes = 2 * 2048;      // of an epilogue warp: two tiles of 32 rows x 64 bytes
+static_assert(kStageBytes >= mxg::kStageBytes && kOffStage % 1024 == 0, "staging");
+constexpr int kSmemBytes = kOffStage + kEpiWarps * kStageBytes + 1024;
 static_assert(kBBytes % 1024 == 0 && kSmemBytes <= 227 * 1024, "shared memory layout");
 
 struct Params {
@@ -77,6 +79,12 @@ __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc,
 // in both CTAs of the pair, each from its own shared memory.
 __device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Wait until at most N bulk stores of this thread still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // Descriptor of such rows: no swizzle, 16-byte rows, groups of eight 128 bytes apart.
@@ -180,7 +188,8 @@ struct ScaleItem {
 // ------------------------------------------------------------------ the kernel
 
 __global__ void __launch_bounds__(kThreads, 1)
-    a4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
+    a4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+              const __grid_constant__ CUtensorMap tm_y, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sb = smem + kOffB, *ss = smem + kOffS;
@@ -385,10 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         pdl_wait();
         Ring acc;
-        const uint32_t stage = smem_u32(smem + kOffStage) + (warp - 4) * mxg::kStageBytes;
+        // A warp's tile of 32 rows x 32 outputs leaves by TMA from shared memory (two in flight a warp):
+        // stores of a row a lane occupy the load/store unit for a cache line a lane, which delayed the
+        // issuing warp's barrier tests.  Rows that do not start on 16-byte boundaries: write_ragged.
+        uint8_t *tile = smem + kOffStage + (warp - 4) * kStageBytes;
+        const bool ragged = p.o.J & 7;
+        int buffer = 0;
         for (int t = t0; t < t1; ++t) {
-            const long long m = static_cast<long long>(row_of(t)) + quarter * 32 + lane;
-            const int j0 = out_of(t);
+            const int m0 = row_of(t) + quarter * 32, j0 = out_of(t);
             if (!mbar_wait(&acc_full[acc.slot], acc.phase)) break;
             tc_fence_after();
             for (int c = c0; c < c0 + half; c += 32) {
@@ -397,15 +410,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(tmem + lanes + acc.slot * kAccCols + c, r);
                 tmem_ld_wait_regs(r);
                 const int j = j0 + c;
-                if (j >= p.o.J) break;
-                if (p.o.J & 7) mxg::write_ragged(p.o, m - lane, j, r, stage, lane);
-                else if (m < p.o.M) mxg::write_columns<mxg::kPlain>(p.o, m, j, r);
+                if (j >= p.o.J || m0 >= p.o.M) break;
+                if (ragged) {
+                    mxg::write_ragged(p.o, m0, j, r, smem_u32(tile), lane);
+                    continue;
+                }
+                if (lane == 0) bulk_wait_read<1>();       // the copy before the last has read its buffer
+                __syncwarp();
+                const uint32_t to = smem_u32(tile) + buffer * 2048 + lane * 64;
+                float v[32];
+#pragma unroll
+                for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sts128(to + ((q ^ ((lane >> 1) & 3)) << 4), mxg::pack8(v + 8 * q));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tm_y, tile + buffer * 2048, j, m0);
+                    bulk_commit_group();
+                }
+                buffer ^= 1;
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc.slot);
             acc.advance(2);
         }
+        if (lane == 0) bulk_wait_all();         // written, and shared memory released
     }
 
     __syncwarp();

@@ -228,8 +228,13 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
     rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, mx4::kStep / 8, p.bn / 2,
                    CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
+    CUtensorMap ty;
+    std::memset(&ty, 0, sizeof(ty));
+    if (N % 8 == 0)
+        rc = encode_2d(d, &ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (rc) return rc;
     const dim3 grid(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)), 1, 1);
-    return mx_launch(mx4::a4_kernel, grid, 2, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, p);
+    return mx_launch(mx4::a4_kernel, grid, 2, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, ty, p);
 }
 
 // Few rows of x take the matvec: up to 16 always, up to 32 where the weight is small.  Measured, us,

@@ -292,179 +292,190 @@ def w4a16_quantize(w, wq=None, scales=None, biases=None, stream=None):
 #
 # wq int32/uint32 [N, K/8] codes and scales uint8 [N, K/32], as in include/w4a16.h.  Tensors are
 # contiguous and on one CUDA device, which need not be the current one; outputs that are not given
-# are allocated there.  The checks run on every call of a decode loop, so they look at each tensor
-# once and build messages only when they fail.
+# are allocated there.  A decode loop runs these functions for every token, so each looks at what it
+# was given in one expression, and only a call that fails it goes on to find out why.
 
 MX_BLOCK = 32
 
+_torch = None            # torch and what the checks compare with, bound by the first call
+_bf16 = _f32 = _i32 = _u32 = _u8 = None
 
-def _mx_fail(name, t, dtype, shape):
+
+def _mx_setup():
+    global _torch, _bf16, _f32, _i32, _u32, _u8
     import torch
-    if not isinstance(t, torch.Tensor):
+    _bf16, _f32, _i32, _u32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint32, torch.uint8
+    _torch = torch
+
+
+def _mx_ok(t, dtype, rows, cols, device):
+    """A contiguous CUDA matrix of this type and shape on this device (by index)."""
+    return t.dtype is dtype and t.shape == (rows, cols) and t.get_device() == device and t.is_contiguous()
+
+
+def _mx_refuse(name, t, dtypes, shape, device=None):
+    """Why a tensor is not what its function needs."""
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dtype != dtype and not (dtype == torch.int32 and t.dtype == torch.uint32):
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}, or is on another device than "
-                     "the first argument")
-
-
-def _mx_need(name, t, dtype, shape, device):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        import torch
-        if not (dtype == torch.int32 and t.dtype == torch.uint32 and t.shape == shape and t.device == device
-                and t.is_contiguous()):
-            _mx_fail(name, t, dtype, shape)
-
-
-def _mx_rows(name, t, dtypes):
-    """(rows, columns, device) of a 2-D CUDA tensor whose columns are a whole number of blocks or
-    are checked by the caller."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}")
-    return t.shape[0], t.shape[1], t.device
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device} like the first argument")
 
 
-def _mx_out(name, t, dtype, shape, device, stream):
+def _mx_rows(name, t, *dtypes):
+    """Rows, columns and device of the first argument (bfloat16 unless types are given)."""
+    if _torch is None:
+        _mx_setup()
+    if not dtypes:
+        dtypes = (_bf16,)
+    if not (isinstance(t, _torch.Tensor) and t.dtype in dtypes and t.is_cuda and t.dim() == 2 and t.is_contiguous()):
+        _mx_refuse(name, t, dtypes, None)
+    rows, cols = t.shape
+    return rows, cols, t.get_device()
+
+
+def _mx_weights(wq, scales, K, device, names=("wq", "scales")):
+    """Rows N of stored codes [N, K/8] with their scales [N, K/32]."""
+    if K % MX_BLOCK:
+        raise W4A16Error(ERR_UNSUPPORTED, f"rows of {K} values: K must be a multiple of {MX_BLOCK}")
+    if not isinstance(wq, _torch.Tensor) or wq.dim() != 2:
+        _mx_refuse(names[0], wq, (_i32, _u32), None)
+    N = wq.shape[0]
+    if not (_mx_ok(wq, _i32, N, K // 8, device) or _mx_ok(wq, _u32, N, K // 8, device)):
+        _mx_refuse(names[0], wq, (_i32, _u32), (N, K // 8), device)
+    if not (isinstance(scales, _torch.Tensor) and _mx_ok(scales, _u8, N, K // MX_BLOCK, device)):
+        _mx_refuse(names[1], scales, (_u8,), (N, K // MX_BLOCK), device)
+    return N
+
+
+def _mx_out(name, t, like, dtype, rows, cols, device, stream):
     """A given output, checked, or a new one; new memory that another stream than its own will
     write is recorded on that stream."""
-    import torch
-    if t is not None:
-        _mx_need(name, t, dtype, shape, device)
-        return t
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device))
+    if t is None:
+        t = like.new_empty((rows, cols), dtype=dtype)
+        if stream is not None:
+            t.record_stream(stream if hasattr(stream, "cuda_stream")
+                            else _torch.cuda.ExternalStream(int(stream), device))
+    elif not (isinstance(t, _torch.Tensor) and (_mx_ok(t, dtype, rows, cols, device) or (
+            dtype is _i32 and _mx_ok(t, _u32, rows, cols, device)))):
+        _mx_refuse(name, t, (_i32, _u32) if dtype is _i32 else (dtype,), (rows, cols), device)
     return t
 
 
-def _mx_call(name, device, stream, *args):
-    """Runs a C entry point on `device` (made current for the call) and its stream."""
-    import torch
-    index = device.index
-    fn = getattr(lib, name)
+def _mx_run(fn, device, stream, *args):
+    """Calls a C entry point on `device`, made current for the call, and its stream."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
+        handle = _torch._C._cuda_getCurrentRawStream(device)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index == torch._C._cuda_getDevice():
+    if device == _torch._C._cuda_getDevice():
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(index):
+        with _torch.cuda.device(device):
             status = fn(*args, handle)
     if status != OK:
-        raise W4A16Error(status, name)
-
-
-def _mx_weights(wq, scales, K, device):
-    """N of stored weights [N, K/8], [N, K/32]."""
-    import torch
-    if K % MX_BLOCK:
-        raise W4A16Error(ERR_UNSUPPORTED, f"rows of {K} values: K must be a multiple of {MX_BLOCK}")
-    if wq.dim() != 2:
-        raise ValueError("wq must be 2-D")
-    N = wq.shape[0]
-    _mx_need("wq", wq, torch.int32, (N, K // 8), device)
-    _mx_need("scales", scales, torch.uint8, (N, K // MX_BLOCK), device)
-    return N
+        raise W4A16Error(status, fn.__name__)
 
 
 def w4a16_mx_quantize(w, wq=None, scales=None, stream=None):
     """Quantise w [N, K] (float32 or bfloat16: weights, or activations for w4a16_mx_matmul_a4) to
     MXFP4: returns (wq int32 [N, K/8], scales uint8 [N, K/32])."""
-    import torch
-    N, K, device = _mx_rows("w", w, (torch.float32, torch.bfloat16))
+    if _torch is None:
+        _mx_setup()
+    N, K, device = _mx_rows("w", w, _f32, _bf16)
     if K % MX_BLOCK:
         raise W4A16Error(ERR_UNSUPPORTED, "w4a16_mx_quantize")
-    wq = _mx_out("wq", wq, torch.int32, (N, K // 8), device, stream)
-    scales = _mx_out("scales", scales, torch.uint8, (N, K // MX_BLOCK), device, stream)
-    _mx_call("w4a16_mx_quantize", device, stream, w.data_ptr(), DTYPE_F32 if w.dtype == torch.float32 else DTYPE_BF16,
-             wq.data_ptr(), scales.data_ptr(), N, K)
+    wq = _mx_out("wq", wq, w, _i32, N, K // 8, device, stream)
+    scales = _mx_out("scales", scales, w, _u8, N, K // MX_BLOCK, device, stream)
+    _mx_run(lib.w4a16_mx_quantize, device, stream, w.data_ptr(), DTYPE_F32 if w.dtype is _f32 else DTYPE_BF16,
+            wq.data_ptr(), scales.data_ptr(), N, K)
     return wq, scales
 
 
 def w4a16_mx_dequantize(wq, scales, w=None, dtype=None, stream=None):
     """The values of stored codes [N, K], bfloat16 (default) or float32; both hold them exactly."""
-    import torch
-    N, words, device = _mx_rows("wq", wq, (torch.int32, torch.uint32))
+    if _torch is None:
+        _mx_setup()
+    N, words, device = _mx_rows("wq", wq, _i32, _u32)
     K = words * 8
     _mx_weights(wq, scales, K, device)
-    dtype = (torch.bfloat16 if w is None else w.dtype) if dtype is None else dtype
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype is None:
+        dtype = _bf16 if w is None else w.dtype
+    if dtype is not _f32 and dtype is not _bf16:
         raise TypeError("values come in float32 or bfloat16")
-    w = _mx_out("w", w, dtype, (N, K), device, stream)
-    _mx_call("w4a16_mx_dequantize", device, stream, wq.data_ptr(), scales.data_ptr(), w.data_ptr(),
-             DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16, N, K)
+    w = _mx_out("w", w, wq, dtype, N, K, device, stream)
+    _mx_run(lib.w4a16_mx_dequantize, device, stream, wq.data_ptr(), scales.data_ptr(), w.data_ptr(),
+            DTYPE_F32 if dtype is _f32 else DTYPE_BF16, N, K)
     return w
 
 
 def w4a16_mx_matmul(x, wq, scales, y=None, stream=None):
     """y [M, N] = x . W^T for W in MXFP4; x and y bfloat16, any M."""
-    import torch
-    M, K, device = _mx_rows("x", x, (torch.bfloat16,))
+    M, K, device = _mx_rows("x", x)
     N = _mx_weights(wq, scales, K, device)
-    y = _mx_out("y", y, torch.bfloat16, (M, N), device, stream)
-    _mx_call("w4a16_mx_matmul", device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K)
+    y = _mx_out("y", y, x, _bf16, M, N, device, stream)
+    _mx_run(lib.w4a16_mx_matmul, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K)
     return y
 
 
 def w4a16_mx_matmul_a4(xq, xscales, wq, scales, y=None, stream=None):
     """y [M, N] = X . W^T with both operands in MXFP4 (X from w4a16_mx_quantize of the activations)."""
-    import torch
-    M, words, device = _mx_rows("xq", xq, (torch.int32, torch.uint32))
+    if _torch is None:
+        _mx_setup()
+    M, words, device = _mx_rows("xq", xq, _i32, _u32)
     K = words * 8
-    _mx_weights(xq, xscales, K, device)
+    _mx_weights(xq, xscales, K, device, ("xq", "xscales"))
     N = _mx_weights(wq, scales, K, device)
-    y = _mx_out("y", y, torch.bfloat16, (M, N), device, stream)
-    _mx_call("w4a16_mx_matmul_a4", device, stream, xq.data_ptr(), xscales.data_ptr(), wq.data_ptr(), scales.data_ptr(),
-             y.data_ptr(), M, N, K)
+    y = _mx_out("y", y, xq, _bf16, M, N, device, stream)
+    _mx_run(lib.w4a16_mx_matmul_a4, device, stream, xq.data_ptr(), xscales.data_ptr(), wq.data_ptr(), scales.data_ptr(),
+            y.data_ptr(), M, N, K)
     return y
 
 
 def w4a16_mx_gate_up(x, wq, scales, h=None, stream=None):
     """Gated block, any M: h [M, N2] = bf16(silu(x . gate^T) * (x . up^T)), the two layers' rows
     interleaved in blocks of 8 (interleave_gate_up) in wq and scales (2 N2 rows)."""
-    import torch
-    M, K, device = _mx_rows("x", x, (torch.bfloat16,))
+    M, K, device = _mx_rows("x", x)
     N = _mx_weights(wq, scales, K, device)
     if N % 16:
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
-    h = _mx_out("h", h, torch.bfloat16, (M, N // 2), device, stream)
-    _mx_call("w4a16_mx_gate_up", device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), h.data_ptr(), M, N // 2, K)
+    h = _mx_out("h", h, x, _bf16, M, N // 2, device, stream)
+    _mx_run(lib.w4a16_mx_gate_up, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), h.data_ptr(), M, N // 2, K)
     return h
 
 
 def w4a16_mx_matmul_backward(dy, wq, scales, dx=None, stream=None):
     """The input's gradient of w4a16_mx_matmul: dx [M, K] = dy [M, N] . W; N a multiple of 8."""
-    import torch
-    M, N, device = _mx_rows("dy", dy, (torch.bfloat16,))
-    if wq.dim() != 2:
-        raise ValueError("wq must be 2-D")
+    M, N, device = _mx_rows("dy", dy)
+    if not isinstance(wq, _torch.Tensor) or wq.dim() != 2:
+        _mx_refuse("wq", wq, (_i32, _u32), None)
     K = wq.shape[1] * 8
     if _mx_weights(wq, scales, K, device) != N:
         raise ValueError(f"dy has {N} columns, W {wq.shape[0]} rows")
-    dx = _mx_out("dx", dx, torch.bfloat16, (M, K), device, stream)
-    _mx_call("w4a16_mx_matmul_backward", device, stream, dy.data_ptr(), wq.data_ptr(), scales.data_ptr(), dx.data_ptr(),
-             M, N, K)
+    dx = _mx_out("dx", dx, dy, _bf16, M, K, device, stream)
+    _mx_run(lib.w4a16_mx_matmul_backward, device, stream, dy.data_ptr(), wq.data_ptr(), scales.data_ptr(), dx.data_ptr(),
+            M, N, K)
     return dx
 
 
 def w4a16_mx_gate_up_backward(x, wq, scales, dh, dx=None, dgu=None, stream=None):
     """Backward pass of w4a16_mx_gate_up from x and dh [M, N2]: returns (dx [M, K], dgu [M, 2 N2]),
     dgu the gradients of both projections' outputs with columns interleaved like the rows of W."""
-    import torch
-    M, K, device = _mx_rows("x", x, (torch.bfloat16,))
+    M, K, device = _mx_rows("x", x)
     N = _mx_weights(wq, scales, K, device)
     if N % 16:
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
-    _mx_need("dh", dh, torch.bfloat16, (M, N // 2), device)
-    dx = _mx_out("dx", dx, torch.bfloat16, (M, K), device, stream)
-    dgu = _mx_out("dgu", dgu, torch.bfloat16, (M, N), device, stream)
-    _mx_call("w4a16_mx_gate_up_backward", device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), dh.data_ptr(),
-             dgu.data_ptr(), dx.data_ptr(), M, N // 2, K)
+    if not (isinstance(dh, _torch.Tensor) and _mx_ok(dh, _bf16, M, N // 2, device)):
+        _mx_refuse("dh", dh, (_bf16,), (M, N // 2), device)
+    dx = _mx_out("dx", dx, x, _bf16, M, K, device, stream)
+    dgu = _mx_out("dgu", dgu, x, _bf16, M, N, device, stream)
+    _mx_run(lib.w4a16_mx_gate_up_backward, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), dh.data_ptr(),
+            dgu.data_ptr(), dx.data_ptr(), M, N // 2, K)
     return dx, dgu
 
 

@@ -38,11 +38,15 @@ int mx_sizes(int64_t M, int64_t N, int64_t K) {
 }
 
 using MxGemm = void(const CUtensorMap, const CUtensorMap, const mxg::Params);
+template <bool PAIR>
 MxGemm *mx_gemm_of(bool backward, int epilogue) {
-    if (backward) return mxg::gemm_kernel<true, mxg::kPlain>;
-    if (epilogue == mxg::kGated) return mxg::gemm_kernel<false, mxg::kGated>;
-    if (epilogue == mxg::kGatedBackward) return mxg::gemm_kernel<false, mxg::kGatedBackward>;
-    return mxg::gemm_kernel<false, mxg::kPlain>;
+    if (backward) return mxg::gemm_kernel<true, mxg::kPlain, PAIR>;
+    if (epilogue == mxg::kGated) return mxg::gemm_kernel<false, mxg::kGated, PAIR>;
+    if (epilogue == mxg::kGatedBackward) return mxg::gemm_kernel<false, mxg::kGatedBackward, PAIR>;
+    return mxg::gemm_kernel<false, mxg::kPlain, PAIR>;
+}
+MxGemm *mx_gemm_of(bool backward, int epilogue, bool pair) {
+    return pair ? mx_gemm_of<true>(backward, epilogue) : mx_gemm_of<false>(backward, epilogue);
 }
 
 cudaLaunchAttribute mx_cluster(int ctas) {
@@ -60,21 +64,22 @@ int mx_device(DeviceInfo **d) {
     if (!rc) rc = device_setup(dev, d);
     if (rc || (*d)->mx_ready) return rc;
     cudaError_t e = cudaSuccess;
-    for (MxGemm *kernel : {mx_gemm_of(false, mxg::kPlain), mx_gemm_of(false, mxg::kGated),
-                           mx_gemm_of(false, mxg::kGatedBackward), mx_gemm_of(true, mxg::kPlain)})
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
+    for (bool pair : {false, true})
+        for (MxGemm *kernel : {mx_gemm_of(false, mxg::kPlain, pair), mx_gemm_of(false, mxg::kGated, pair),
+                               mx_gemm_of(false, mxg::kGatedBackward, pair), mx_gemm_of(true, mxg::kPlain, pair)})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mx4::a4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mx4::kSmemBytes);
-    for (int S = 1; S <= mxg::kMaxSplits && e == cudaSuccess; S *= 2) {
+    for (int ctas = 1; ctas <= 2 * mxg::kMaxSplits && e == cudaSuccess; ctas *= 2) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * S, 1, 1);
+        cfg.gridDim = dim3(ctas, 1, 1);
         cfg.blockDim = dim3(mxg::kThreads, 1, 1);
         cfg.dynamicSmemBytes = mxg::kSmemBudget;
-        cudaLaunchAttribute cl = mx_cluster(2 * S);
+        cudaLaunchAttribute cl = mx_cluster(ctas);
         cfg.attrs = &cl;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[S], mx_gemm_of(true, mxg::kPlain), &cfg);
+        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[ctas], mx_gemm_of(true, mxg::kPlain, ctas > 1), &cfg);
     }
     if (e != cudaSuccess) return cuda_fail(e);
     (*d)->mx_ready = true;
@@ -116,25 +121,32 @@ mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilo
     return o;
 }
 
-// Outputs of a CTA pair (bn) and pairs that share a tile's contraction (splits): the least estimated
-// time in SM cycles.  A stage takes its eight MMAs (half a cycle an output, and about 52 cycles
-// at least) or the expanding of a CTA's codes; a persistent grid runs rounds of tiles, a split one has
-// to fit the device at once and pays for the exchange of sums.
+// CTAs work in pairs on 256 rows, or alone on 128 where there are no more (64 rows x 9728 x 2560: 14.3 us
+// alone, 16.5 in pairs).  The outputs of a tile (bn) and how many pairs or CTAs share its contraction
+// (splits) are those of the least estimated time in SM cycles: a stage takes its eight MMAs (half a
+// cycle an output, and about 52 cycles at least) or the expanding of a CTA's codes (measured: 450
+// cycles and 3.25 an output); a persistent grid runs rounds of tiles, a split one has to fit the
+// device at once and pays for the exchange of sums.
 struct MxShape {
+    bool pair = true;
     int bn = 0, splits = 1;
 };
 MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragged, const DeviceInfo *d) {
-    const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows), steps = (C + mxg::kStep - 1) / mxg::kStep;
+    const int64_t steps = (C + mxg::kStep - 1) / mxg::kStep;
     MxShape best;
     int64_t cost = 0;
-    for (int bn = 64; bn <= (ragged ? mxg::kMaxRaggedBN : mxg::kMaxBN); bn += backward ? 64 : 32) {
+    best.pair = M > mxg::kRows;
+    const int ctas = best.pair ? 2 : 1;
+    const int64_t tm = (M + ctas * mxg::kRows - 1) / (ctas * mxg::kRows);
+    const int most = ctas == 1 ? 128 : (ragged ? mxg::kMaxRaggedBN : mxg::kMaxBN);
+    for (int bn = 32 * ctas; bn <= most; bn += backward || ctas == 1 ? 32 * ctas : 32) {
         const int64_t tiles = tm * ((J + bn - 1) / bn);
-        const int64_t mma = 8 * std::max(bn / 2, 52) + 60, stage = std::max<int64_t>(mma, 400 + bn);
+        const int64_t stage = std::max(8 * std::max(bn / 2, 52) + 60, 450 + 13 * bn / (4 * ctas));
         for (int S = 1; S <= mxg::kMaxSplits; S *= 2) {
-            const int64_t room = std::min<int64_t>(d->mx_clusters[S], d->sms / (2 * S));
+            const int64_t room = std::min<int64_t>(d->mx_clusters[ctas * S], d->sms / (ctas * S));
             if (S > 1 && (tiles > room || steps < 2 * S)) continue;
             const int64_t rounds = S > 1 ? 1 : (tiles + room - 1) / room;
-            const int64_t c = rounds * ((steps + S - 1) / S) * stage + (S > 1 ? 1500 : 0);
+            const int64_t c = rounds * (((steps + S - 1) / S) * stage + 500) + (S > 1 ? 3000 + 1000 * S : 0);
             if (!best.bn || c <= cost) {
                 best.bn = bn;
                 best.splits = S;
@@ -157,11 +169,12 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     p.ks = static_cast<int>(K / mx::kBlock);
     p.bn = shape.bn;
     p.splits = shape.splits;
-    const int64_t tm = (M + 2 * mxg::kRows - 1) / (2 * mxg::kRows), tiles = tm * ((J + p.bn - 1) / p.bn);
+    const int ctas = shape.pair ? 2 : 1;
+    const int64_t tm = (M + ctas * mxg::kRows - 1) / (ctas * mxg::kRows), tiles = tm * ((J + p.bn - 1) / p.bn);
     if (tiles >= kSizeLimit) return W4A16_ERR_UNSUPPORTED;
     p.tiles_m = static_cast<int>(tm);
     p.tiles = static_cast<int>(tiles);
-    const int half = p.bn / 2;
+    const int half = p.bn / ctas;
     p.b_bytes = backward ? (half + 63) / 64 * mxg::kGroupBytes : half * mxg::kStep * 2;
     p.w_bytes = half * mxg::kStep / 2;
     p.w_pitch = backward ? half / 2 : mxg::kStep / 2;
@@ -186,9 +199,9 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : mxg::kStep / 8,
                    backward ? mxg::kStep : half, swz);
     if (rc) return rc;
-    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, d->mx_clusters[1]);
-    const dim3 grid(static_cast<unsigned>(2 * p.splits * clusters), 1, 1);
-    return mx_launch(mx_gemm_of(backward, epilogue), grid, 2 * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
+    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, d->mx_clusters[ctas]);
+    const dim3 grid(static_cast<unsigned>(ctas * p.splits * clusters), 1, 1);
+    return mx_launch(mx_gemm_of(backward, epilogue, shape.pair), grid, ctas * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
 }
 
 // Outputs of a CTA pair of the 4-bit product: the fewest column-rounds of the persistent grid; an MMA

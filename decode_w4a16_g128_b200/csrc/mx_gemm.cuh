@@ -310,7 +310,7 @@ __device__ __forceinline__ void st_dsmem_v4(uint32_t cluster_addr, uint4 v) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <bool BACKWARD, int EPILOGUE>
+template <bool BACKWARD, int EPILOGUE, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -323,20 +323,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert((5 * kStages + 4) * 8 + 8 <= kBarBytes, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t cluster_rank = cluster_ctarank();       // 2 split + rank in the pair
-    const uint32_t rank = cluster_rank & 1u, lead = cluster_rank & ~1u;
+    constexpr int kCtas = PAIR ? 2 : 1;              // of a tile (and split)
+    const uint32_t cluster_rank = cluster_ctarank();       // kCtas split + rank in the pair
+    const uint32_t rank = PAIR ? cluster_rank & 1u : 0u, lead = cluster_rank - rank;
     const bool leader = rank == 0;
-    const int all_steps = (p.C + kStep - 1) / kStep, split = static_cast<int>(cluster_rank >> 1);
+    const int all_steps = (p.C + kStep - 1) / kStep, split = static_cast<int>(cluster_rank) / kCtas;
     const int step0 = static_cast<int>(static_cast<long long>(split) * all_steps / p.splits);
     const int steps = static_cast<int>(static_cast<long long>(split + 1) * all_steps / p.splits) - step0;
-    const int half = p.bn / 2;                       // outputs that this CTA expands
-    // tiles of this pair: first, first + pairs, ... (one tile with splits)
-    const int pairs = static_cast<int>(gridDim.x) / (2 * p.splits), first = static_cast<int>(blockIdx.x) / (2 * p.splits);
+    const int half = p.bn / kCtas;                   // outputs that this CTA expands
+    constexpr int kTileRows = kCtas * kRows;
+    // tiles of this pair (or CTA): first, first + pairs, ... (one tile with splits)
+    const int pairs = static_cast<int>(gridDim.x) / (kCtas * p.splits), first = static_cast<int>(blockIdx.x) / (kCtas * p.splits);
 
     if (threadIdx.x == 0) {
         pdl_launch_dependents();
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&ready[i], 1 + kTeamWarps + 1);
+            mbar_init(&ready[i], 1 + kTeamWarps + (PAIR ? 1 : 0));
             mbar_init(&empty[i], 1);
             mbar_init(&expd[i], kTeamWarps);
             mbar_init(&w_full[i], 1);
@@ -344,13 +346,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 2 * kEpiWarps);
+            mbar_init(&acc_empty[i], kCtas * kEpiWarps);
         }
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc_pair(tmem_slot, kTmemCols);
-        tmem_relinquish_pair();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(tmem_slot, kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, kTmemCols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     cluster_sync_all();
@@ -370,13 +377,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long issued = 0;
         bool ok = true;
         for (int t = first; t < p.tiles && ok; t += pairs) {
-            const int row = (t % p.tiles_m) * 2 * kRows + static_cast<int>(rank) * kRows;
+            const int row = (t % p.tiles_m) * kTileRows + static_cast<int>(rank) * kRows;
             for (int i = 0; i < steps; ++i) {
                 if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
-                if (leader) mbar_arrive_expect_tx(&ready[st.slot], 2 * kABytes);   // both CTAs' rows
+                if (leader) mbar_arrive_expect_tx(&ready[st.slot], kCtas * kABytes);   // both CTAs' rows
                 uint8_t *dst = sa + st.slot * kABytes;
-                tma_load_2d_pair(dst, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep, row);
-                tma_load_2d_pair(dst + kABytes / 2, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep + 64, row);
+                if constexpr (PAIR) {
+                    tma_load_2d_pair(dst, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep, row);
+                    tma_load_2d_pair(dst + kABytes / 2, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep + 64, row);
+                } else {
+                    tma_load_2d(dst, &tm_x, &ready[st.slot], (step0 + i) * kStep, row);
+                    tma_load_2d(dst + kABytes / 2, &tm_x, &ready[st.slot], (step0 + i) * kStep + 64, row);
+                }
                 ++issued;
                 st.advance(kStages);
             }
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
             mbar_wait(&w_full[j % kStages], static_cast<uint32_t>((j / kStages) & 1), false);
-    } else if (warp == kWarpForward && lane == 0 && !leader) {
+    } else if (PAIR && warp == kWarpForward && lane == 0 && !leader) {
         // ---------------------------------------------------------------- "expanded", to the leader
         // The arrival has the default (CTA) scope: the expanding warps' writes reached shared memory before
         // their own arrivals, and a cluster-scope release drains the SM's memory pipeline, about a
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // executes some dozens of instructions, and the tensor pipe idles for as long as they take:
         // no busy warp shares its scheduler.
         const bool issuer = elect_one();
-        const uint32_t idesc = umma_idesc_bf16(2 * kRows, p.bn) | (BACKWARD ? kIdescBMnMajor : 0u);
+        const uint32_t idesc = umma_idesc_bf16(kTileRows, p.bn) | (BACKWARD ? kIdescBMnMajor : 0u);
         const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sa));
         const uint64_t b_desc0 = BACKWARD ? desc_mn_sw128(smem_u32(sb)) : umma_desc_sw128(smem_u32(sb));
         const int a_hop = kABytes >> 4, b_hop = p.b_bytes >> 4;
@@ -447,14 +459,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (issuer) {
                     const uint64_t ad = a_desc0 + st.slot * a_hop, bd = b_desc0 + st.slot * b_hop;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_pair(d, ad + (kk >> 2) * (kABytes >> 5) + 2 * (kk & 3), bd + (kk >> 2) * b_half + kBHop * (kk & 3),
-                                       idesc, kk > 0 || i > 0);
-                    umma_commit_pair(&empty[st.slot], pair_mask);
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint64_t ak = ad + (kk >> 2) * (kABytes >> 5) + 2 * (kk & 3);
+                        const uint64_t bk = bd + (kk >> 2) * b_half + kBHop * (kk & 3);
+                        if constexpr (PAIR) umma_bf16_pair(d, ak, bk, idesc, kk > 0 || i > 0);
+                        else umma_bf16(d, ak, bk, idesc, kk > 0 || i > 0);
+                    }
+                    if constexpr (PAIR) umma_commit_pair(&empty[st.slot], pair_mask);
+                    else umma_commit(&empty[st.slot]);
                 }
                 st.advance(kStages);
             }
-            if (ok && issuer) umma_commit_pair(&acc_full[acc.slot], pair_mask);
+            if (ok && issuer) {
+                if constexpr (PAIR) umma_commit_pair(&acc_full[acc.slot], pair_mask);
+                else umma_commit(&acc_full[acc.slot]);
+            }
             acc.advance(2);
         }
     } else if (warp >= 8 && (warp & 3) != 1) {
@@ -537,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t v[32];
             tmem_ld32(tmem + lanes + 32 * c, v);
             tmem_ld_wait_regs(v);
-            const uint32_t base = dsmem_addr(smem_u32(smem), 2 * to + rank) + ((split * own + c / S) * 8 * kRows + row) * 16;
+            const uint32_t base = dsmem_addr(smem_u32(smem), kCtas * to + rank) + ((split * own + c / S) * 8 * kRows + row) * 16;
 #pragma unroll
             for (int q = 0; q < 8; ++q) st_dsmem_v4(base + q * kRows * 16, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
         }
@@ -549,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         pdl_wait();
         Ring acc;
         for (int t = first; t < p.tiles; t += pairs) {
-            const long long m = static_cast<long long>(t % p.tiles_m) * 2 * kRows + rank * kRows + row;
+            const long long m = static_cast<long long>(t % p.tiles_m) * kTileRows + rank * kRows + row;
             const int j0 = t / p.tiles_m * p.bn;
             if (S == 1 && !mbar_wait(&acc_full[acc.slot], acc.phase)) break;
             tc_fence_after();
@@ -588,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == kWarpMma) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, kTmemCols);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+        else tmem_dealloc(tmem, kTmemCols);
     }
     __syncwarp();
     cluster_sync_all();   // no CTA leaves while its peer may still signal it

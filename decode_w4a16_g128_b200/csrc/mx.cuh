@@ -26,6 +26,53 @@ __device__ __forceinline__ float code_f32(uint32_t c) {
     return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * __uint_as_float(253u << 23);
 }
 
+// ------------------------------------------------------------------ codes to BF16
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A scale byte as BF16 factors: a code's three low bits in BF16's lowest exponent bits and highest
+// mantissa bit are its magnitude times 2^-126 (code 1 as a subnormal), so the factor is 2^(e - 1).
+// Above e = 128 that is beyond BF16: there the factor is 2^127, and the rest, 2^(e - 128) or NaN, a
+// second one.
+constexpr uint32_t kOneFactor = 128;       // largest scale byte with one factor
+__device__ __forceinline__ uint32_t factor_of(uint32_t e) { return e * 0x00800080u + 126u * 0x00800080u; }
+__device__ __forceinline__ uint32_t second_factor_of(uint32_t e) {
+    return e == kScaleNan ? 0x7FC07FC0u : (e - 1u) * 0x00800080u;
+}
+
+// Eight codes, lowest k first -> four BF16 pairs, lowest k first, times the factor.  Codes 2i and 2i + 1
+// go to the two halves of a register (the selector's sign-replicating bytes are zero there: every byte
+// is below 128), one multiplication by 2^12 + 2^6 puts the sign bit to bit 15 and the others to bits 6-8.
+__device__ __forceinline__ void expand8(uint32_t v, uint32_t f, uint32_t (&r)[4]) {
+    const uint32_t lo = v & 0x0F0F0F0Fu, hi = (v >> 4) & 0x0F0F0F0Fu;
+    r[0] = prmt(lo, hi, 0xC480u);
+    r[1] = prmt(lo, hi, 0xD591u);
+    r[2] = prmt(lo, hi, 0xE6A2u);
+    r[3] = prmt(lo, hi, 0xF7B3u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2((r[i] * 0x1040u) & 0x81C081C0u, f);
+}
+
+// ------------------------------------------------------------------ stores of 32 bytes
+
+__device__ __forceinline__ void store32(uint16_t *dst, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+__device__ __forceinline__ void store_pair(uint16_t *dst, uint4 a, uint4 b, bool wide) {
+    if (wide) {
+        store32(dst, a, b);
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = a;
+        reinterpret_cast<uint4 *>(dst)[1] = b;
+    }
+}
+
 // ------------------------------------------------------------------ quantiser
 //
 // Per block: top = the largest magnitude, e = max(0, floor(log2 top) - 2 + 127), so that top lands in
@@ -123,40 +170,51 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const void *w, uint
 // Every value is exact in BF16 (two significant bits; 2^-128 is one of its subnormals) unless it
 // is beyond FP32's range too, where it becomes an infinity.  Bound: HBM.
 
+// Eight codes to 16 bytes of BF16 values.
+__device__ __forceinline__ uint4 values_bf16(uint32_t c, uint32_t e) {
+    uint32_t r[4];
+    expand8(c, factor_of(min(e, kOneFactor)), r);
+    if (e > kOneFactor) {
+        const uint32_t more = second_factor_of(e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = mul_bf16x2(r[j], more);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+constexpr int kDUnroll = 2;
+
+// pairs: pairs of code words in all (blocks have two).
 template <bool BF16>
-__global__ void __launch_bounds__(kQThreads) dequantize_kernel(const uint32_t *wq, const uint8_t *scales, void *w,
-                                                               long long words) {
+__global__ void __launch_bounds__(kQThreads) dequantize_kernel(const uint2 *wq, const uint8_t *scales, void *w, bool wide,
+                                                               long long pairs) {
     pdl_launch_dependents();
     pdl_wait();
-    const long long stride = static_cast<long long>(gridDim.x) * kQThreads * kQUnroll;
-    for (long long base = (static_cast<long long>(blockIdx.x) * kQUnroll) * kQThreads + threadIdx.x; base < words;
+    const long long stride = static_cast<long long>(gridDim.x) * kQThreads * kDUnroll;
+    for (long long base = (static_cast<long long>(blockIdx.x) * kDUnroll) * kQThreads + threadIdx.x; base < pairs;
          base += stride) {
-        uint32_t c[kQUnroll], e[kQUnroll];
+        uint2 c[kDUnroll];
+        uint32_t e[kDUnroll];
 #pragma unroll
-        for (int u = 0; u < kQUnroll; ++u) {
+        for (int u = 0; u < kDUnroll; ++u) {
             const long long i = base + u * kQThreads;
-            c[u] = i < words ? __ldcs(wq + i) : 0u;
-            e[u] = i < words ? scales[i >> 2] : 0u;
+            c[u] = i < pairs ? __ldcs(wq + i) : make_uint2(0u, 0u);
+            e[u] = i < pairs ? scales[i >> 1] : 0u;
         }
 #pragma unroll
-        for (int u = 0; u < kQUnroll; ++u) {
+        for (int u = 0; u < kDUnroll; ++u) {
             const long long i = base + u * kQThreads;
-            if (i >= words) break;
-            const float s = scale_f32(e[u]);
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = code_f32(c[u] >> (4 * j)) * s;
+            if (i >= pairs) break;
             if constexpr (BF16) {
-                uint4 o;
-                o.x = pack_bf16x2(v[0], v[1]);
-                o.y = pack_bf16x2(v[2], v[3]);
-                o.z = pack_bf16x2(v[4], v[5]);
-                o.w = pack_bf16x2(v[6], v[7]);
-                static_cast<uint4 *>(w)[i] = o;
+                store_pair(static_cast<uint16_t *>(w) + 16 * i, values_bf16(c[u].x, e[u]), values_bf16(c[u].y, e[u]), wide);
             } else {
-                float4 *o = static_cast<float4 *>(w) + 2 * i;
-                o[0] = make_float4(v[0], v[1], v[2], v[3]);
-                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                const float s = scale_f32(e[u]);
+                float4 *o = static_cast<float4 *>(w) + 4 * i;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t d = (q < 2 ? c[u].x : c[u].y) >> (16 * (q & 1));
+                    o[q] = make_float4(code_f32(d) * s, code_f32(d >> 4) * s, code_f32(d >> 8) * s, code_f32(d >> 12) * s);
+                }
             }
         }
     }

@@ -290,9 +290,10 @@ int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *w
     return mx_matvec_launch<1, 4, 8, 1, 2>(p, stream);
 }
 
-unsigned stream_grid(int64_t words, int sms) {
-    const int64_t per = int64_t(mx::kQThreads) * mx::kQUnroll;
-    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((words + per - 1) / per, int64_t(sms) * 8)));
+// CTAs of a streaming kernel whose threads take `unroll` items each at a time.
+unsigned stream_grid(int64_t items, int unroll, int sms) {
+    const int64_t per = int64_t(mx::kQThreads) * unroll;
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((items + per - 1) / per, int64_t(sms) * 8)));
 }
 
 }  // namespace
@@ -314,7 +315,7 @@ int w4a16_mx_quantize(const void *w, int32_t w_dtype, uint32_t *wq, uint8_t *sca
     rc = mx_device(&d);
     if (rc) return rc;
     const long long words = N * (K / 8);
-    const dim3 grid(stream_grid(words, d->sms), 1, 1);
+    const dim3 grid(stream_grid(words, mx::kQUnroll, d->sms), 1, 1);
     if (w_dtype == W4A16_DTYPE_BF16)
         return mx_launch(mx::quantize_kernel<true>, grid, 1, mx::kQThreads, 0, stream, w, wq, scales, words);
     return mx_launch(mx::quantize_kernel<false>, grid, 1, mx::kQThreads, 0, stream, w, wq, scales, words);
@@ -333,11 +334,13 @@ int w4a16_mx_dequantize(const uint32_t *wq, const uint8_t *scales, void *w, int3
     DeviceInfo *d = nullptr;
     rc = mx_device(&d);
     if (rc) return rc;
-    const long long words = N * (K / 8);
-    const dim3 grid(stream_grid(words, d->sms), 1, 1);
+    const long long pairs = N * (K / 16);
+    const dim3 grid(stream_grid(pairs, mx::kDUnroll, d->sms), 1, 1);
+    const auto *codes = reinterpret_cast<const uint2 *>(wq);
+    const bool wide = (reinterpret_cast<uintptr_t>(w) & 31u) == 0;
     if (w_dtype == W4A16_DTYPE_BF16)
-        return mx_launch(mx::dequantize_kernel<true>, grid, 1, mx::kQThreads, 0, stream, wq, scales, w, words);
-    return mx_launch(mx::dequantize_kernel<false>, grid, 1, mx::kQThreads, 0, stream, wq, scales, w, words);
+        return mx_launch(mx::dequantize_kernel<true>, grid, 1, mx::kQThreads, 0, stream, codes, scales, w, wide, pairs);
+    return mx_launch(mx::dequantize_kernel<false>, grid, 1, mx::kQThreads, 0, stream, codes, scales, w, wide, pairs);
 }
 
 int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, void *y, int64_t M, int64_t N, int64_t K,

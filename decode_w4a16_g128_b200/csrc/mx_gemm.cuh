@@ -97,57 +97,12 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t smem_addr) {
 }
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
-// ------------------------------------------------------------------ codes to BF16
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// A scale byte as BF16 factors: a code's three low bits in BF16's lowest exponent bits and highest
-// mantissa bit are its magnitude times 2^-126 (code 1 as a subnormal), so the factor is 2^(e - 1).
-// Above e = 128 that is beyond BF16: there the factor is 2^127, and the rest, 2^(e - 128) or NaN, a
-// second one.
-constexpr uint32_t kOneFactor = 128;       // largest scale byte with one factor
-__device__ __forceinline__ uint32_t factor_of(uint32_t e) { return e * 0x00800080u + 126u * 0x00800080u; }
-__device__ __forceinline__ uint32_t second_factor_of(uint32_t e) {
-    return e == mx::kScaleNan ? 0x7FC07FC0u : (e - 1u) * 0x00800080u;
-}
-
-// Eight codes, lowest k first -> four BF16 pairs, lowest k first, times the factor.  Codes 2i and 2i + 1
-// go to the two halves of a register (the selector's sign-replicating bytes are zero there: every byte
-// is below 128), one multiplication by 2^12 + 2^6 puts the sign bit to bit 15 and the others to bits 6-8.
-__device__ __forceinline__ void expand8(uint32_t v, uint32_t f, uint32_t (&r)[4]) {
-    const uint32_t lo = v & 0x0F0F0F0Fu, hi = (v >> 4) & 0x0F0F0F0Fu;
-    r[0] = prmt(lo, hi, 0xC480u);
-    r[1] = prmt(lo, hi, 0xD591u);
-    r[2] = prmt(lo, hi, 0xE6A2u);
-    r[3] = prmt(lo, hi, 0xF7B3u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2((r[i] * 0x1040u) & 0x81C081C0u, f);
-}
-
 // ------------------------------------------------------------------ epilogue helpers
 
 // Eight or sixteen values to BF16 at 16- or 32-byte boundaries.
 __device__ __forceinline__ uint4 pack8(const float *v) {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-__device__ __forceinline__ void store32(uint16_t *dst, uint4 a, uint4 b) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
-                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
-}
-__device__ __forceinline__ void store_pair(uint16_t *dst, uint4 a, uint4 b, bool wide) {
-    if (wide) {
-        store32(dst, a, b);
-    } else {
-        reinterpret_cast<uint4 *>(dst)[0] = a;
-        reinterpret_cast<uint4 *>(dst)[1] = b;
-    }
-}
-
 // Where a product's sums go: BF16 of them [M, J], silu(gate) up [M, J/2], or both gradients [M, J].
 enum Epilogue { kPlain = 0, kGated = 1, kGatedBackward = 2 };
 struct Output {
@@ -167,7 +122,7 @@ __device__ __forceinline__ void write_columns(const Output &p, long long m, int 
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * q + i]);
-            if (j + 16 * q + 8 < p.J) store_pair(dst + 16 * q, pack8(v), pack8(v + 8), p.wide);
+            if (j + 16 * q + 8 < p.J) mx::store_pair(dst + 16 * q, pack8(v), pack8(v + 8), p.wide);
             else if (j + 16 * q < p.J) *reinterpret_cast<uint4 *>(dst + 16 * q) = pack8(v);
         }
     } else if constexpr (EPILOGUE == kGated) {    // J is a multiple of 16: 8 gate columns and their 8 up columns
@@ -181,7 +136,7 @@ __device__ __forceinline__ void write_columns(const Output &p, long long m, int 
                 a[i] = mx::gated(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]));
             o[q] = pack8(a);
         }
-        if (j + 16 < p.J) store_pair(dst, o[0], o[1], p.wide);
+        if (j + 16 < p.J) mx::store_pair(dst, o[0], o[1], p.wide);
         else *reinterpret_cast<uint4 *>(dst) = o[0];
     } else {
         const uint16_t *src = p.dh + m * (p.J / 2) + j / 2;
@@ -195,7 +150,7 @@ __device__ __forceinline__ void write_columns(const Output &p, long long m, int 
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 mx::gated_backward(__uint_as_float(r[16 * q + i]), __uint_as_float(r[16 * q + 8 + i]), dh[i], a[i], b[i]);
-            store_pair(p.out + m * p.J + j + 16 * q, pack8(a), pack8(b), p.wide);
+            mx::store_pair(p.out + m * p.J + j + 16 * q, pack8(a), pack8(b), p.wide);
         }
     }
 }
@@ -282,23 +237,23 @@ __device__ __forceinline__ uint32_t scales_of(uint2 v, int row, int blk, int ks)
 
 // A block of 32 codes -> 64 bytes of BF16 at `to`, the first of four swizzled 16-byte chunks.
 __device__ __forceinline__ void expand_block(const uint4 &c, uint32_t to, uint32_t e) {
-    const uint32_t f = factor_of(min(e, kOneFactor));
+    const uint32_t f = mx::factor_of(min(e, mx::kOneFactor));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    if (e <= kOneFactor) {
+    if (e <= mx::kOneFactor) {
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             uint32_t v[4];
-            expand8(w[jj], f, v);
+            mx::expand8(w[jj], f, v);
             sts128(to ^ (jj << 4), make_uint4(v[0], v[1], v[2], v[3]));
         }
     } else {
-        const uint32_t more = second_factor_of(e);
+        const uint32_t more = mx::second_factor_of(e);
 #pragma unroll 1
         for (int jj = 0; jj < 4; ++jj) {
             uint32_t v[4];
-            expand8(jj == 0 ? c.x : (jj == 1 ? c.y : (jj == 2 ? c.z : c.w)), f, v);
-            sts128(to ^ (jj << 4), make_uint4(mul_bf16x2(v[0], more), mul_bf16x2(v[1], more), mul_bf16x2(v[2], more),
-                                              mul_bf16x2(v[3], more)));
+            mx::expand8(jj == 0 ? c.x : (jj == 1 ? c.y : (jj == 2 ? c.z : c.w)), f, v);
+            sts128(to ^ (jj << 4), make_uint4(mx::mul_bf16x2(v[0], more), mx::mul_bf16x2(v[1], more), mx::mul_bf16x2(v[2], more),
+                                              mx::mul_bf16x2(v[3], more)));
         }
     }
 }

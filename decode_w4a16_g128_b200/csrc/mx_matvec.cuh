@@ -15,7 +15,7 @@
 // of D groups are in flight a warp.  Bound: memory latency and L2; the whole weight is one pass.
 #pragma once
 
-#include "mx_gemm.cuh"
+#include "mx.cuh"
 
 namespace w4a16 {
 namespace mxv {
@@ -39,10 +39,10 @@ __device__ __forceinline__ void expand_pairs(uint32_t v, uint32_t f, uint32_t mo
     r[2] = (u & 0x000F000Fu) * 0x1040u;
     r[3] = (u & 0x00F000F0u) * 0x0104u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i] & 0x81C081C0u, f);
+    for (int i = 0; i < 4; ++i) r[i] = mx::mul_bf16x2(r[i] & 0x81C081C0u, f);
     if (more) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = mxg::mul_bf16x2(r[i], more);
+        for (int i = 0; i < 4; ++i) r[i] = mx::mul_bf16x2(r[i], more);
     }
 }
 
@@ -100,8 +100,8 @@ __device__ __forceinline__ void multiply(const Codes<RB> &st, const Rows<NB> &x,
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            f[rb][h] = mxg::factor_of(min(st.e[rb][h], mxg::kOneFactor));
-            more[rb][h] = st.e[rb][h] > mxg::kOneFactor ? mxg::second_factor_of(st.e[rb][h]) : 0u;
+            f[rb][h] = mx::factor_of(min(st.e[rb][h], mx::kOneFactor));
+            more[rb][h] = st.e[rb][h] > mx::kOneFactor ? mx::second_factor_of(st.e[rb][h]) : 0u;
         }
 #pragma unroll
     for (int w = 0; w < 4; ++w) {

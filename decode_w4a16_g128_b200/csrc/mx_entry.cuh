@@ -11,7 +11,8 @@
 namespace w4a16 {
 namespace {
 
-constexpr int64_t kSizeLimit = int64_t(1) << 31;
+// Row numbers of partial tiles and of stages asked for ahead stay below 2^31.
+constexpr int64_t kSizeLimit = (int64_t(1) << 31) - 65536;
 
 struct Span {
     const void *p;
@@ -143,7 +144,7 @@ MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragge
         const int64_t tiles = tm * ((J + bn - 1) / bn);
         const int64_t stage = std::max(8 * std::max(bn / 2, 52) + 60, 450 + 13 * bn / (4 * ctas));
         for (int S = 1; S <= mxg::kMaxSplits; S *= 2) {
-            const int64_t room = std::min<int64_t>(d->mx_clusters[ctas * S], d->sms / (ctas * S));
+            const int64_t room = std::max<int64_t>(1, std::min<int64_t>(d->mx_clusters[ctas * S], d->sms / (ctas * S)));
             if (S > 1 && (tiles > room || steps < 2 * S)) continue;
             const int64_t rounds = S > 1 ? 1 : (tiles + room - 1) / room;
             const int64_t c = rounds * (((steps + S - 1) / S) * stage + 500) + (S > 1 ? 3000 + 1000 * S : 0);
@@ -199,7 +200,7 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : mxg::kStep / 8,
                    backward ? mxg::kStep : half, swz);
     if (rc) return rc;
-    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, d->mx_clusters[ctas]);
+    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, d->mx_clusters[ctas]));
     const dim3 grid(static_cast<unsigned>(ctas * p.splits * clusters), 1, 1);
     return mx_launch(mx_gemm_of(backward, epilogue, shape.pair), grid, ctas * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
 }
@@ -335,12 +336,14 @@ int w4a16_mx_dequantize(const uint32_t *wq, const uint8_t *scales, void *w, int3
     rc = mx_device(&d);
     if (rc) return rc;
     const long long pairs = N * (K / 16);
-    const dim3 grid(stream_grid(pairs, mx::kDUnroll, d->sms), 1, 1);
+    const int unroll = pairs >= (1 << 20) ? 4 : 2;
+    const dim3 grid(stream_grid(pairs, unroll, d->sms), 1, 1);
     const auto *codes = reinterpret_cast<const uint2 *>(wq);
     const bool wide = (reinterpret_cast<uintptr_t>(w) & 31u) == 0;
-    if (w_dtype == W4A16_DTYPE_BF16)
-        return mx_launch(mx::dequantize_kernel<true>, grid, 1, mx::kQThreads, 0, stream, codes, scales, w, wide, pairs);
-    return mx_launch(mx::dequantize_kernel<false>, grid, 1, mx::kQThreads, 0, stream, codes, scales, w, wide, pairs);
+    const auto kernel = w_dtype == W4A16_DTYPE_BF16
+                            ? (unroll == 4 ? mx::dequantize_kernel<true, 4> : mx::dequantize_kernel<true, 2>)
+                            : (unroll == 4 ? mx::dequantize_kernel<false, 4> : mx::dequantize_kernel<false, 2>);
+    return mx_launch(kernel, grid, 1, mx::kQThreads, 0, stream, codes, scales, w, wide, pairs);
 }
 
 int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, void *y, int64_t M, int64_t N, int64_t K,

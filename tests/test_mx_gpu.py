@@ -241,6 +241,100 @@ def test_gate_up_backward_against_differences():
     near(dx, num, bound + (ref.sum_error(dgu, w.T)))
 
 
+# Sizes at which the kernels take their other shapes: several rounds of tiles a CTA, every tile width,
+# a contraction shared by two or four CTAs or pairs, single CTAs, rows that start at odd addresses.
+# The reference is a product of whole numbers in 64 bits on the GPU.
+LARGE = [(2048, 4104, 544), (257, 19456, 96), (640, 5001, 640), (129, 333, 9728), (128, 19456, 256), (64, 4096, 2560),
+         (100, 151, 8192), (1000, 10007, 512), (2047, 2056, 1312), (512, 1000, 9728), (40, 2560, 9728), (300, 9728, 160)]
+
+
+def whole_on_gpu(rng, rows, k):
+    x = torch.from_numpy(rng.integers(-8, 9, (rows, k)).astype(np.float32)).cuda()
+    return x.bfloat16(), x.double()
+
+
+def values_on_gpu(wq, s):
+    return w4.w4a16_mx_dequantize(wq, s, dtype=torch.float32).double()
+
+
+def equal(got, want):
+    bad = got != want.float().bfloat16()
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} differ, first at {bad.nonzero()[:4].tolist()}"
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_exact(M, N, K):
+    rng = np.random.default_rng([20, M, N, K])
+    wq, s = dev(*ref.random_stored(rng, N, K, 126, 128))
+    w = values_on_gpu(wq, s)
+    x, xd = whole_on_gpu(rng, M, K)
+    y = xd @ w.T                                   # multiples of 1/4 below 2^22: exact in FP32 too
+    equal(w4.w4a16_mx_matmul(x, wq, s), y)
+    xq, xs = w4.w4a16_mx_quantize(x)               # whole numbers up to 8: blocks of scale 1 or 2
+    equal(w4.w4a16_mx_matmul_a4(xq, xs, wq, s), values_on_gpu(xq, xs) @ w.T)
+    if N % 8 == 0:
+        dy, dyd = whole_on_gpu(rng, M, N)
+        equal(w4.w4a16_mx_matmul_backward(dy, wq, s), dyd @ w)
+    assert w4.w4a16_device_status() == w4.OK
+
+
+@pytest.mark.parametrize("M,N,K", [(2048, 2056, 544), (509, 9728, 256), (128, 9728, 256), (64, 1000, 2560), (17, 4864, 96)])
+def test_large_gated(M, N, K):
+    rng = np.random.default_rng([21, M, N, K])
+    wq, s = ref.random_stored(rng, 2 * N, K, 119, 121)
+    wq, s = dev(wq, s)
+    w = values_on_gpu(wq, s)
+    x, xd = whole_on_gpu(rng, M, K)
+    dh, dhd = whole_on_gpu(rng, M, N)
+    gu = (xd @ w.T).reshape(M, -1, 2, 8)           # exact in FP32: multiples of 2^-9, below 2^9
+    g, u = gu[:, :, 0], gu[:, :, 1]
+    t = torch.sigmoid(g)
+    scalar = (4 + 1.173 * g.abs()) * 2.0 ** -23 + 12 * 2.0 ** -24     # see mx_reference.scalar
+
+    def close(got, want, err):
+        bad = (got.double() - want).abs() > ref.HALF_STEP * (want.abs() + err) + err + ref.TINY
+        assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[:4].tolist()}"
+
+    h = g * t * u
+    close(w4.w4a16_mx_gate_up(x, wq, s), h.reshape(M, N), (scalar * h.abs()).reshape(M, N))
+    dx, dgu = w4.w4a16_mx_gate_up_backward(x, wq, s, dh)
+    d = dhd.reshape(M, -1, 8)
+    dg, du = d * u * t * (1 + g * (1 - t)), d * g * t
+    eg = scalar * d.abs() * u.abs() * t * (1 + 2 * g.abs())
+    close(dgu, torch.stack([dg, du], 2).reshape(M, 2 * N), torch.stack([eg, scalar * du.abs()], 2).reshape(M, 2 * N))
+    want = dgu.double() @ w
+    err = (2 * N / 16 + 32) * 2.0 ** -23 * (dgu.double().abs() @ w.abs())
+    close(dx, want, err)
+    assert w4.w4a16_device_status() == w4.OK
+
+
+def test_first_call_of_a_process_captured():
+    """No call needs a warm-up before it is captured, not even the first one on the device."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, decode_w4a16_g128_b200 as w4
+x = torch.ones(40, 64, dtype=torch.bfloat16, device="cuda")
+w = torch.ones(32, 64, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    wq, s = w4.w4a16_mx_quantize(w)
+    y = w4.w4a16_mx_matmul(x, wq, s)
+    h = w4.w4a16_mx_gate_up(x, wq, s)
+    y4 = w4.w4a16_mx_matmul_a4(*w4.w4a16_mx_quantize(x), wq, s)
+    dx, dgu = w4.w4a16_mx_gate_up_backward(x, wq, s, h)
+    v = w4.w4a16_mx_dequantize(wq, s)
+g.replay()
+torch.cuda.synchronize()
+assert (y == 64).all() and (y4 == 64).all() and (h == 4096).all() and (v == 1).all(), (y, y4, h, v)
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stdout + out.stderr
+
+
 # ------------------------------------------------------------------ empty and odd calls
 
 

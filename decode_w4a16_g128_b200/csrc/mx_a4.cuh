@@ -20,6 +20,9 @@
 // Roles (512 threads): warp 0 codes by TMA, warp 1 MMA issue (leader) and tensor memory, warps 2, 3, 12,
 // 14 and 15 scales (with two loader warps their instructions took longer than the MMAs), warps 4-11
 // epilogue; warp 13 would share the issuing warp's scheduler and stays idle.
+//
+// Bound, 2048 x 9728 x 2560: 32.7 us (3.12 PFLOP/s; the tensor pipe is active 47 % of the time, no other
+// unit more than 35 %).  A stage's MMAs take 384 cycles and its turn of the issue loop 525 to 670.
 #pragma once
 
 #include "mx_gemm.cuh"
@@ -212,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto out_of = [&](int t) { return t % p.tiles_n * p.bn; };
 
     if (threadIdx.x == 0) {
-        pdl_launch_dependents();
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ready[i], 1);           // codes of both CTAs
             mbar_init(&empty[i], 1);
@@ -234,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    if (threadIdx.x == 0) pdl_launch_dependents();   // what starts early cannot take the tensor memory first
     const uint32_t tmem = *tmem_slot;
     const uint32_t ready_l = dsmem_addr(smem_u32(ready), 0), acc_empty_l = dsmem_addr(smem_u32(acc_empty), 0);
     const uint32_t s_full_l = dsmem_addr(smem_u32(s_full), 0);
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring st, sp, acc;
             int done = 0;
             bool ok = true;
+            pdl_wait();
             for (int t = t0; t < t1 && ok; ++t, ++done) {
                 if (done >= 2 && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
                 tc_fence_after();
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int buffer = 0;
         for (int t = t0; t < t1; ++t) {
             const int m0 = row_of(t) + quarter * 32, j0 = out_of(t);
-            if (!mbar_wait(&acc_full[acc.slot], acc.phase)) break;
+            if (!mbar_wait(&acc_full[acc.slot], acc.phase, true, mxg::tile_limit_ns(steps))) break;
             tc_fence_after();
             for (int c = c0; c < c0 + half; c += 32) {
                 __syncwarp();                   // the loads are collective

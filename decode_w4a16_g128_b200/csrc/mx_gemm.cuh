@@ -18,15 +18,20 @@
 // run of the stages; their partial sums meet in shared memory over the cluster, added in split order.
 //
 // Roles (768 threads): warp 1 MMA issue (leader) and tensor memory, warps 0, 2-7 and 21 epilogue,
-// twelve of warps 8-23 expand codes in three teams, and beside warp 1 on its scheduler one warp that copies codes, one
-// that copies x, and the peer's that forwards "expanded" to the leader.  The ring has three stages, one
-// a team.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's four expanding warps, the peer's
-// forwarder), empty[s] (both CTAs; the stage's MMAs completed), exp[s] (peer: its four expanding
-// warps), w_full[s] / w_empty[s] (codes), acc_full / acc_empty (accumulators).
+// twelve of warps 8-23 expand codes in three teams, and beside warp 1 on its scheduler one warp that
+// copies codes, one that copies x, and the peer's that forwards "expanded" to the leader.  The ring has
+// three stages, one a team.  Barriers: ready[s] (leader; x bytes of both CTAs, the leader's four
+// expanding warps, the peer's forwarder), empty[s] (both CTAs; the stage's MMAs completed), expd[s] (peer:
+// its four expanding warps), w_full[s] / w_empty[s] (codes), acc_full / acc_empty (accumulators).  No
+// waiter is a whole ring behind what it waits for: a team's next stage is in the same slot, so it has
+// waited for this one's MMAs, and the parities never alias.
 //
-// What the stage's length and the roles' places were measured to be worth (2048 x 9728 x 2560, forward):
-// the MMAs of K = 64 a stage take less time than the dozens of instructions around a stage's waits
-// do in a crowded SM, and the tensor pipe idles meanwhile.
+// Bound, forward, 2048 x 9728 x 2560: 73 us (1.40 PFLOP/s; the tensor pipe is active 72 % of the time, the
+// integer pipe 43 %, issue slots 47 %, DRAM 4 %).  What is left is the time between two stages' MMAs: with
+// stages of K = 64, whose MMAs take less time than the instructions around a stage's waits do in a crowded
+// SM, the same product took 84 us.  Backward, 2048 x 9728 x 2560: 86 us, 112 tiles of 192 outputs on 74
+// pairs, so a third of the last round's pairs have none.  Few rows (33 - 128 x 9728 x 2560): 14.3 us,
+// two rounds of tiles on single CTAs, a stage as long as its codes take to expand.
 #pragma once
 
 #include "mx.cuh"
@@ -58,6 +63,9 @@ __host__ __device__ constexpr int smem_bytes(int b_bytes, int w_bytes, bool ragg
 static_assert(smem_bytes(kMaxBN / 2 * kStep * 2, kMaxBN / 2 * kStep / 2, false) <= kSmemBudget &&
               smem_bytes(kMaxRaggedBN / 2 * kStep * 2, kMaxRaggedBN / 2 * kStep / 2, true) <= kSmemBudget,
               "shared memory budget");
+// Two of these kernels, or one and the other tensor-core kernels, never share an SM: each takes all of
+// its tensor memory, and a CTA that waited for it might hold what the other needs.
+static_assert(2 * smem_bytes(32 * kStep * 2, 32 * kStep / 2, false) > 228 * 1024, "one CTA an SM");
 
 // ------------------------------------------------------------------ PTX
 
@@ -199,6 +207,11 @@ struct Ring {
     }
 };
 
+// Limit of a wait for a whole tile: one of 2^31 values a row takes seconds.
+__device__ __forceinline__ unsigned long long tile_limit_ns(int steps) {
+    return kWaitTimeoutNs + 4000ull * static_cast<unsigned long long>(steps);
+}
+
 // ------------------------------------------------------------------ scale bytes
 
 // Up to four scale bytes of a stored row from block `blk` on: the aligned words that hold them (the
@@ -291,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pairs = static_cast<int>(gridDim.x) / (kCtas * p.splits), first = static_cast<int>(blockIdx.x) / (kCtas * p.splits);
 
     if (threadIdx.x == 0) {
-        pdl_launch_dependents();
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ready[i], 1 + kTeamWarps + (PAIR ? 1 : 0));
             mbar_init(&empty[i], 1);
@@ -317,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    if (threadIdx.x == 0) pdl_launch_dependents();   // what starts early cannot take the tensor memory first
     const uint32_t tmem = *tmem_slot;
     const uint32_t ready_l = dsmem_addr(smem_u32(ready), lead), acc_empty_l = dsmem_addr(smem_u32(acc_empty), lead);
     const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
@@ -380,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // microsecond a stage.
         Ring st;
         bool ok = true;
+        pdl_wait();
         for (int t = first; t < p.tiles && ok; t += pairs)
             for (int i = 0; i < steps && ok; ++i) {
                 ok = mbar_wait(&expd[st.slot], st.phase);
@@ -404,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring st, acc;
         int done = 0;
         bool ok = true;
+        pdl_wait();
         for (int t = first; t < p.tiles && ok; t += pairs, ++done) {
             // the accumulator's previous tile has been read
             if (done >= 2 && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
@@ -491,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (epilogue && p.splits > 1) {
-        mbar_wait(&acc_full[0], 0);
+        pdl_wait();
+        mbar_wait(&acc_full[0], 0, true, tile_limit_ns(steps));
     }
 
     const int quarter = warp & 3, chunks = p.bn / 32, S = p.splits, own = (chunks + S - 1) / S;
@@ -525,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = first; t < p.tiles; t += pairs) {
             const long long m = static_cast<long long>(t % p.tiles_m) * kTileRows + rank * kRows + row;
             const int j0 = t / p.tiles_m * p.bn;
-            if (S == 1 && !mbar_wait(&acc_full[acc.slot], acc.phase)) break;
+            if (S == 1 && !mbar_wait(&acc_full[acc.slot], acc.phase, true, tile_limit_ns(steps))) break;
             tc_fence_after();
             for (int c = split + S * epi_set; c < chunks; c += 2 * S) {
                 __syncwarp();                   // the loads are collective

@@ -326,6 +326,8 @@ int w4a16_matmul_bits(const void *x, const uint32_t *wq, const void *scales,
  *
  * Numerics: every stored value is exact in BF16, every product exact in FP32; sums are FP32 (order
  * fixed by the sizes and the device model, so results repeat bit for bit), rounded once to BF16.
+ * Values of 2^128 and more (from e = 253 on; the quantiser ends at 252) are infinities; only
+ * w4a16_mx_matmul_a4 may also take them as they are.
  * NaN and infinities in a row of x reach that row's outputs alone; a NaN block of W reaches its
  * row's outputs alone.
  *

@@ -535,3 +535,46 @@ def test_refusals_on_the_device():
     with pytest.raises(w4.W4A16Error) as e:
         w4.w4a16_mx_matmul(x.reshape(-1)[8 * 64 // 16:][:64].view(1, 64).flatten()[0:0].new_zeros(65)[1:].view(1, 64), wq, s)
     assert e.value.status == w4.ERR_MISALIGNED
+
+
+def spread(picked, at, k, stored):
+    """Rows of k values that are zeros but for codes picked [rows, len(at)] at columns `at`."""
+    rows, words = picked.shape[0], [i // 8 for i in at]
+    assert len(set(words)) == len(at)
+    if not stored:
+        x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+        x[:, at] = dev_bf16(ref.GRID[picked])
+        return x
+    wq = torch.zeros(rows, k // 8, dtype=torch.int32, device="cuda")
+    nibbles = picked.astype(np.uint32) << np.array([4 * (i % 8) for i in at], np.uint32)
+    wq[:, words] = torch.from_numpy(nibbles.view(np.int32)).cuda()
+    return wq, torch.full((rows, k // 32), 127, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("M,N,K,op", [(2, 2, 2 ** 31 - 65536 - 32, "matmul"), (2, 2, 2 ** 31 - 65536 - 32, "a4"),
+                                      (40, 8, 2 ** 26, "matmul"), (40, 16, 2 ** 26, "gate_up"),
+                                      (40, 8, 2 ** 26, "backward")])
+def test_long_rows(M, N, K, op):
+    """Up to the longest rows: offsets beyond 2^32 bytes, and a tile that takes seconds."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    at = [0, 39, K // 2 + 8, K - 40, K - 1]
+    rng = np.random.default_rng([21, M, N])
+    px, pw = rng.integers(0, 16, (M, len(at))), rng.integers(0, 16, (N, len(at)))
+    x, w = ref.GRID[px], ref.GRID[pw]
+    wq, s = spread(pw, at, K, True)
+    if op == "matmul":
+        same(host(w4.w4a16_mx_matmul(spread(px, at, K, False), wq, s)), ref.bf16(x @ w.T))
+    elif op == "a4":
+        same(host(w4.w4a16_mx_matmul_a4(*spread(px, at, K, True), wq, s)), ref.bf16(x @ w.T))
+    elif op == "gate_up":
+        h, tol = ref.gate_up(x, w)
+        near(host(w4.w4a16_mx_gate_up(spread(px, at, K, False), wq, s)), h, tol)
+    else:
+        dy = whole(rng, M, N)
+        dx = w4.w4a16_mx_matmul_backward(dev_bf16(dy), wq, s)
+        same(host(dx[:, at]), ref.bf16(dy @ w))
+        dx[:, at] = 0
+        assert not dx.any()
+    torch.cuda.synchronize()
+    assert w4.w4a16_device_status() == 0

@@ -252,43 +252,65 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
 }
 
 // Few rows of x take the matvec: up to 16 always, up to 32 where the weight is small.  Measured, us,
-// matvec / GEMM: M = 16 N x K 9728 x 2560 11.5 / 19.9, 2560 x 9728 15.6 / 20.1; M = 32 1024 x 2560
-// 6.8 / 10.7, 4096 x 2560 9.0 / 12.3, but 2560 x 9728 26.7 / 20.1 and 19456 x 2560 38 / 26.5.
+// matvec / GEMM: M = 16 N x K 9728 x 2560 11.4 / 14.3, 2560 x 9728 15.5 / 17.5; M = 32 1024 x 2560
+// 6.8 / 9.7, 4096 x 2560 8.8 / 11.1, but 2560 x 9728 26.7 / 17.4 and 19456 x 2560 38 / 26.5.
 bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
     return M <= 16 || (M <= mxv::kMaxM && N * K <= (int64_t(1) << 24));
 }
 
-template <int RB, int NB, int WARPS, int D, int CTAS>
+template <int NB, int WARPS, int D, int CTAS, bool X4>
 int mx_matvec_launch(const mxv::Params &p, void *stream) {
-    const dim3 grid(static_cast<unsigned>((int64_t(p.N) + 16 * RB - 1) / (16 * RB)), 1, 1);
-    return mx_launch(mxv::matvec_kernel<RB, NB, WARPS, D, CTAS>, grid, 1, 32 * WARPS, 0, stream, p);
+    const dim3 grid(static_cast<unsigned>((int64_t(p.N) + 15) / 16), 1, 1);
+    return mx_launch(mxv::matvec_kernel<NB, WARPS, D, CTAS, X4>, grid, 1, 32 * WARPS, 0, stream, p);
 }
 
-int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *ws, void *out, int64_t M, int64_t N,
-              int64_t K, bool gated, void *stream) {
-    mxv::Params p;
-    p.x = static_cast<const uint16_t *>(x);
+// Warps of a CTA (they share its rows' K): as many as leave every CTA resident at once, 16 (one
+// CTA an SM), 8 (two) or 4 (five).  Measured at M = 1, us, with 16 / 8 / 4 warps: N x K 2560 x 9728
+// 10.7 / 9.9 / 13.1, 4096 x 2560 5.8 / 4.0 / 5.4, 9728 x 2560 12.4 / 8.7 / 7.0.
+template <bool X4>
+int mx_matvec_8(const mxv::Params &p, const DeviceInfo *d, void *stream) {
+    const int64_t blocks = (int64_t(p.N) + 15) / 16;
+    if (blocks <= d->sms) return mx_matvec_launch<1, 16, 2, 1, X4>(p, stream);
+    if (blocks <= 2 * d->sms) return mx_matvec_launch<1, 8, 2, 2, X4>(p, stream);
+    return mx_matvec_launch<1, 4, 2, 5, X4>(p, stream);
+}
+
+mxv::Params mx_matvec_params(const uint32_t *wq, const uint8_t *ws, void *out, int64_t M, int64_t N, int64_t K) {
+    mxv::Params p = {};
     p.wq = wq;
     p.ws = ws;
     p.out = static_cast<uint16_t *>(out);
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(N);
     p.K = static_cast<int>(K);
+    return p;
+}
+
+int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *ws, void *out, int64_t M, int64_t N,
+              int64_t K, bool gated, void *stream) {
+    mxv::Params p = mx_matvec_params(wq, ws, out, M, N, K);
+    p.x = static_cast<const uint16_t *>(x);
     p.gated = gated ? 1 : 0;
-    // Warps of a CTA (they share its rows' K): as many as leave every CTA resident at once, 16 (one
-    // CTA an SM), 8 (two) or 4 (five).  Measured at M = 1, us, with 16 / 8 / 4 warps: N x K 2560 x 9728
-    // 10.7 / 9.9 / 13.1, 4096 x 2560 5.8 / 4.0 / 5.4, 9728 x 2560 12.4 / 8.7 / 7.0.
-    const int64_t blocks = (N + 15) / 16;
-    if (M <= 8) {
-        if (blocks <= d->sms) return mx_matvec_launch<1, 1, 16, 2, 1>(p, stream);
-        if (blocks <= 2 * d->sms) return mx_matvec_launch<1, 1, 8, 2, 2>(p, stream);
-        return mx_matvec_launch<1, 1, 4, 2, 5>(p, stream);
-    }
+    if (M <= 8) return mx_matvec_8<false>(p, d, stream);
     if (M <= 16) {
-        if (blocks <= 2 * d->sms) return mx_matvec_launch<1, 2, 8, 2, 2>(p, stream);
-        return mx_matvec_launch<1, 2, 4, 1, 5>(p, stream);
+        if ((N + 15) / 16 <= 2 * d->sms) return mx_matvec_launch<2, 8, 2, 2, false>(p, stream);
+        return mx_matvec_launch<2, 4, 1, 5, false>(p, stream);
     }
-    return mx_matvec_launch<1, 4, 8, 1, 2>(p, stream);
+    return mx_matvec_launch<4, 8, 1, 2, false>(p, stream);
+}
+
+// The same with x in 4 bits, for up to 8 rows and small weights: past that the FP4 tensor cores are no
+// slower, as here x is expanded anew for every 16 weight rows.  Measured, us, this / FP4 tensor cores: M = 1
+// N x K 1024 x 2560 4.8 / 8.4, 4096 x 2560 6.5 / 9.0, 1024 x 16384 10.9 / 21.0, 9728 x 2560 9.8 / 10.4; M = 8
+// 4096 x 2560 7.2 / 9.0, 8192 x 2048 8.9 / 8.6; M = 16 6400 x 2560 11.8 / 9.4.
+bool mx_few_a4(int64_t M, int64_t N, int64_t K) { return M <= 8 && N * K <= (int64_t(1) << 24); }
+
+int mx_matvec_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *wq, const uint8_t *ws, void *out,
+                 int64_t M, int64_t N, int64_t K, void *stream) {
+    mxv::Params p = mx_matvec_params(wq, ws, out, M, N, K);
+    p.xq = xq;
+    p.xs = xs;
+    return mx_matvec_8<true>(p, d, stream);
 }
 
 // CTAs of a streaming kernel whose threads take `unroll` items each at a time.
@@ -376,6 +398,7 @@ int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(y, s[0].bytes, stream);
+    if (mx_few_a4(M, N, K)) return mx_matvec_a4(d, xq, xscales, wq, scales, y, M, N, K, stream);
     return mx_a4(d, xq, xscales, wq, scales, y, M, N, K, stream);
 }
 

@@ -72,7 +72,7 @@ int mx_device(DeviceInfo **d) {
                 e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mx4::a4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mx4::kSmemBytes);
-    for (int ctas = 1; ctas <= 2 * mxg::kMaxSplits && e == cudaSuccess; ctas *= 2) {
+    for (int ctas = 1; ctas <= mxg::kMaxCluster && e == cudaSuccess; ++ctas) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(ctas, 1, 1);
         cfg.blockDim = dim3(mxg::kThreads, 1, 1);
@@ -80,7 +80,7 @@ int mx_device(DeviceInfo **d) {
         cudaLaunchAttribute cl = mx_cluster(ctas);
         cfg.attrs = &cl;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[ctas], mx_gemm_of(true, mxg::kPlain, ctas > 1), &cfg);
+        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[ctas], mx_gemm_of(true, mxg::kPlain, false), &cfg);
     }
     if (e != cudaSuccess) return cuda_fail(e);
     (*d)->mx_ready = true;
@@ -122,12 +122,13 @@ mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilo
     return o;
 }
 
-// CTAs work in pairs on 256 rows, or alone on 128 where there are no more (64 rows x 9728 x 2560: 14.3 us
+// CTAs work in pairs on 256 rows, or alone on 128 where there are no more (64 rows x 9728 x 2560: 14.2 us
 // alone, 16.5 in pairs).  The outputs of a tile (bn) and how many pairs or CTAs share its contraction
 // (splits) are those of the least estimated time in SM cycles: a stage takes its eight MMAs (half a
 // cycle an output, and about 52 cycles at least) or the expanding of a CTA's codes (measured: 450
 // cycles and 3.25 an output); a persistent grid runs rounds of tiles, a split one has to fit the
-// device at once and pays for the exchange of sums.
+// device at once and pays for the exchange of sums.  Any number of splits up to a cluster of eight (64
+// rows, gradients of 2 x 9728 x 2560: 50.9 us, 52.8 with powers of two alone).
 struct MxShape {
     bool pair = true;
     int bn = 0, splits = 1;
@@ -143,9 +144,9 @@ MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragge
     for (int bn = 32 * ctas; bn <= most; bn += backward || ctas == 1 ? 32 * ctas : 32) {
         const int64_t tiles = tm * ((J + bn - 1) / bn);
         const int64_t stage = std::max(8 * std::max(bn / 2, 52) + 60, 450 + 13 * bn / (4 * ctas));
-        for (int S = 1; S <= mxg::kMaxSplits; S *= 2) {
+        for (int S = 1; ctas * S <= mxg::kMaxCluster; ++S) {
             const int64_t room = std::max<int64_t>(1, std::min<int64_t>(d->mx_clusters[ctas * S], d->sms / (ctas * S)));
-            if (S > 1 && (tiles > room || steps < 2 * S)) continue;
+            if (S > 1 && (tiles > room || steps < 2 * S || !mxg::sums_fit(bn, ctas, S))) continue;
             const int64_t rounds = S > 1 ? 1 : (tiles + room - 1) / room;
             const int64_t c = rounds * (((steps + S - 1) / S) * stage + 500) + (S > 1 ? 3000 + 1000 * S : 0);
             if (!best.bn || c <= cost) {

@@ -14,8 +14,9 @@
 //      [128 n][64 outputs] per group of 64 outputs, MN-major: the transposition is the descriptor's.
 // Two accumulators of 256 columns fill tensor memory: the epilogue of a tile runs under the next
 // tile's main loop.  The grid is persistent; the host picks BN for the fewest column-rounds (see
-// mx_entry.cuh).  Where the tiles leave SMs idle, S pairs share a tile (a cluster of 2 S CTAs), each a
-// run of the stages; their partial sums meet in shared memory over the cluster, added in split order.
+// mx_entry.cuh).  Where the tiles leave SMs idle, S pairs (or CTAs) share a tile, a cluster of up to
+// eight CTAs, each a run of the stages; their partial sums meet in shared memory over the cluster, added
+// in split order.
 //
 // Roles (768 threads): warp 1 MMA issue (leader) and tensor memory, warps 0, 2-7 and 21 epilogue,
 // twelve of warps 8-23 expand codes in three teams, and beside warp 1 on its scheduler one warp that
@@ -46,7 +47,7 @@ constexpr int kStages = 3;
 constexpr int kABytes = kRows * kStep * 2;
 constexpr int kEpiWarps = 8;
 constexpr int kTeams = kStages, kTeamWarps = 4;   // expanding warps, see there
-constexpr int kMaxSplits = 4;
+constexpr int kMaxCluster = 8;           // CTAs that share a tile
 // Warps with w % 4 == 1 share the issuing warp's scheduler: light roles.
 constexpr int kWarpMma = 1, kWarpCodes = 9, kWarpX = 13, kWarpForward = 17, kWarpEpi = 21;
 constexpr int kTmemCols = 512;
@@ -63,6 +64,10 @@ __host__ __device__ constexpr int smem_bytes(int b_bytes, int w_bytes, bool ragg
 static_assert(smem_bytes(kMaxBN / 2 * kStep * 2, kMaxBN / 2 * kStep / 2, false) <= kSmemBudget &&
               smem_bytes(kMaxRaggedBN / 2 * kStep * 2, kMaxRaggedBN / 2 * kStep / 2, true) <= kSmemBudget,
               "shared memory budget");
+// The S splits' partial sums of a CTA's columns (see there) fit the stages' A and B, S = 1 .. 8.
+__host__ __device__ constexpr bool sums_fit(int bn, int ctas, int S) {
+    return (S * ((bn / 32 + S - 1) / S)) * 32 * kRows * 4 <= kStages * (kABytes + bn / ctas * kStep * 2);
+}
 // Two of these kernels, or one and the other tensor-core kernels, never share an SM: each takes all of
 // its tensor memory, and a CTA that waited for it might hold what the other needs.
 static_assert(2 * smem_bytes(32 * kStep * 2, 32 * kStep / 2, false) > 228 * 1024, "one CTA an SM");

@@ -50,7 +50,7 @@ struct DeviceInfo {
     int gemm_clusters = 0;    // CTA pairs of the GEMM resident at once (its persistent grid)
     int gemm_max_splits = 4;  // K splits of the GEMM: 8 where clusters of 16 CTAs can be resident
     bool mx_ready = false;    // the MXFP4 kernels' attributes are set
-    int mx_clusters[9] = {};  // clusters of 1, 2, 4 and 8 CTAs of the MXFP4 GEMM resident at once
+    int mx_clusters[9] = {};  // clusters of 1 .. 8 CTAs of the MXFP4 GEMM resident at once
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 

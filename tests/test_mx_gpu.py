@@ -242,10 +242,12 @@ def test_gate_up_backward_against_differences():
 
 
 # Sizes at which the kernels take their other shapes: several rounds of tiles a CTA, every tile width,
-# a contraction shared by two or four CTAs or pairs, single CTAs, rows that start at odd addresses.
+# a contraction shared by up to eight CTAs or four pairs, single CTAs, rows that start at odd addresses.
 # The reference is a product of whole numbers in 64 bits on the GPU.
 LARGE = [(2048, 4104, 544), (257, 19456, 96), (640, 5001, 640), (129, 333, 9728), (128, 19456, 256), (64, 4096, 2560),
-         (100, 151, 8192), (1000, 10007, 512), (2047, 2056, 1312), (512, 1000, 9728), (40, 2560, 9728), (300, 9728, 160)]
+         (100, 151, 8192), (1000, 10007, 512), (2047, 2056, 1312), (512, 1000, 9728), (40, 2560, 9728), (300, 9728, 160),
+         (40, 1280, 4096), (40, 640, 9728), (40, 1000, 16384), (40, 2048, 16384), (300, 1600, 4096), (300, 2048, 4096),
+         (300, 4096, 2560), (40, 16384, 992), (64, 9728, 640)]
 
 
 def whole_on_gpu(rng, rows, k):

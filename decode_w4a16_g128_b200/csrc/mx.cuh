@@ -57,6 +57,17 @@ __device__ __forceinline__ void expand8(uint32_t v, uint32_t f, uint32_t (&r)[4]
     for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2((r[i] * 0x1040u) & 0x81C081C0u, f);
 }
 
+// The same, codes i and i + 4 as pair i: they lie 16 bits apart already, which saves the selections.
+__device__ __forceinline__ void expand8_apart(uint32_t v, uint32_t f, uint32_t (&r)[4]) {
+    const uint32_t u = v >> 8;
+    r[0] = (v & 0x000F000Fu) * 0x1040u;
+    r[1] = (v & 0x00F000F0u) * 0x0104u;
+    r[2] = (u & 0x000F000Fu) * 0x1040u;
+    r[3] = (u & 0x00F000F0u) * 0x0104u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i] & 0x81C081C0u, f);
+}
+
 // ------------------------------------------------------------------ stores of 32 bytes
 
 __device__ __forceinline__ void store32(uint16_t *dst, uint4 a, uint4 b) {

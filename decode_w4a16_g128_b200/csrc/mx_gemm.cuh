@@ -253,7 +253,10 @@ __device__ __forceinline__ uint32_t scales_of(uint2 v, int row, int blk, int ks)
     return e;
 }
 
-// A block of 32 codes -> 64 bytes of BF16 at `to`, the first of four swizzled 16-byte chunks.
+// A block of 32 codes -> 64 bytes of BF16 at `to`, the first of four swizzled 16-byte chunks.  Codes along
+// the contraction keep their order, which is that of x; codes along the outputs (APART) stay in the order
+// that costs least, and the epilogue renames the columns (backward, 64 rows: see there).
+template <bool APART>
 __device__ __forceinline__ void expand_block(const uint4 &c, uint32_t to, uint32_t e) {
     const uint32_t f = mx::factor_of(min(e, mx::kOneFactor));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -261,7 +264,8 @@ __device__ __forceinline__ void expand_block(const uint4 &c, uint32_t to, uint32
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             uint32_t v[4];
-            mx::expand8(w[jj], f, v);
+            if constexpr (APART) mx::expand8_apart(w[jj], f, v);
+            else mx::expand8(w[jj], f, v);
             sts128(to ^ (jj << 4), make_uint4(v[0], v[1], v[2], v[3]));
         }
     } else {
@@ -269,7 +273,9 @@ __device__ __forceinline__ void expand_block(const uint4 &c, uint32_t to, uint32
 #pragma unroll 1
         for (int jj = 0; jj < 4; ++jj) {
             uint32_t v[4];
-            mx::expand8(jj == 0 ? c.x : (jj == 1 ? c.y : (jj == 2 ? c.z : c.w)), f, v);
+            const uint32_t word = jj == 0 ? c.x : (jj == 1 ? c.y : (jj == 2 ? c.z : c.w));
+            if constexpr (APART) mx::expand8_apart(word, f, v);
+            else mx::expand8(word, f, v);
             sts128(to ^ (jj << 4), make_uint4(mx::mul_bf16x2(v[0], more), mx::mul_bf16x2(v[1], more), mx::mul_bf16x2(v[2], more),
                                               mx::mul_bf16x2(v[3], more)));
         }
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (filled && !mbar_wait(&empty[team], phase ^ 1u)) { ok = false; break; }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (src[q]) expand_block(c[q], dst[q], (e >> (8 * (b0 + q * share))) & 255u);
+                    if (src[q]) expand_block<BACKWARD>(c[q], dst[q], (e >> (8 * (b0 + q * share))) & 255u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -563,6 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + __uint_as_float(o.y));
                         v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + __uint_as_float(o.z));
                         v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + __uint_as_float(o.w));
+                    }
+                }
+                if constexpr (BACKWARD) {       // columns 2 i and 2 i + 1 of eight hold outputs i and i + 4
+#pragma unroll
+                    for (int g = 0; g < 32; g += 8) {
+                        const uint32_t t[8] = {v[g], v[g + 2], v[g + 4], v[g + 6], v[g + 1], v[g + 3], v[g + 5], v[g + 7]};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[g + i] = t[i];
                     }
                 }
                 const int j = j0 + 32 * c;

@@ -38,13 +38,7 @@ struct Params {
 
 // Codes j and j + 4 of a word -> BF16 pairs times the factor (`more`: a second one, 0 for none).
 __device__ __forceinline__ void expand_pairs(uint32_t v, uint32_t f, uint32_t more, uint32_t (&r)[4]) {
-    const uint32_t u = v >> 8;
-    r[0] = (v & 0x000F000Fu) * 0x1040u;
-    r[1] = (v & 0x00F000F0u) * 0x0104u;
-    r[2] = (u & 0x000F000Fu) * 0x1040u;
-    r[3] = (u & 0x00F000F0u) * 0x0104u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = mx::mul_bf16x2(r[i] & 0x81C081C0u, f);
+    mx::expand8_apart(v, f, r);
     if (more) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = mx::mul_bf16x2(r[i], more);

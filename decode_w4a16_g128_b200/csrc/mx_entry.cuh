@@ -39,15 +39,21 @@ int mx_sizes(int64_t M, int64_t N, int64_t K) {
 }
 
 using MxGemm = void(const CUtensorMap, const CUtensorMap, const mxg::Params);
-template <bool PAIR>
+template <bool PAIR, int SHARE>
 MxGemm *mx_gemm_of(bool backward, int epilogue) {
-    if (backward) return mxg::gemm_kernel<true, mxg::kPlain, PAIR>;
-    if (epilogue == mxg::kGated) return mxg::gemm_kernel<false, mxg::kGated, PAIR>;
-    if (epilogue == mxg::kGatedBackward) return mxg::gemm_kernel<false, mxg::kGatedBackward, PAIR>;
-    return mxg::gemm_kernel<false, mxg::kPlain, PAIR>;
+    if (backward) return mxg::gemm_kernel<true, mxg::kPlain, PAIR, SHARE>;
+    if (epilogue == mxg::kGated) return mxg::gemm_kernel<false, mxg::kGated, PAIR, SHARE>;
+    if (epilogue == mxg::kGatedBackward) return mxg::gemm_kernel<false, mxg::kGatedBackward, PAIR, SHARE>;
+    return mxg::gemm_kernel<false, mxg::kPlain, PAIR, SHARE>;
 }
-MxGemm *mx_gemm_of(bool backward, int epilogue, bool pair) {
-    return pair ? mx_gemm_of<true>(backward, epilogue) : mx_gemm_of<false>(backward, epilogue);
+template <bool PAIR>
+MxGemm *mx_gemm_of(bool backward, int epilogue, int share) {
+    if (share == mxg::kNone) return mx_gemm_of<PAIR, mxg::kNone>(backward, epilogue);
+    if (share == mxg::kLast) return mx_gemm_of<PAIR, mxg::kLast>(backward, epilogue);
+    return mx_gemm_of<PAIR, mxg::kAll>(backward, epilogue);
+}
+MxGemm *mx_gemm_of(bool backward, int epilogue, bool pair, int share) {
+    return pair ? mx_gemm_of<true>(backward, epilogue, share) : mx_gemm_of<false>(backward, epilogue, share);
 }
 
 cudaLaunchAttribute mx_cluster(int ctas) {
@@ -66,10 +72,12 @@ int mx_device(DeviceInfo **d) {
     if (rc || (*d)->mx_ready) return rc;
     cudaError_t e = cudaSuccess;
     for (bool pair : {false, true})
-        for (MxGemm *kernel : {mx_gemm_of(false, mxg::kPlain, pair), mx_gemm_of(false, mxg::kGated, pair),
-                               mx_gemm_of(false, mxg::kGatedBackward, pair), mx_gemm_of(true, mxg::kPlain, pair)})
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
+        for (int share : {mxg::kNone, mxg::kLast, mxg::kAll})
+            for (MxGemm *kernel :
+                 {mx_gemm_of(false, mxg::kPlain, pair, share), mx_gemm_of(false, mxg::kGated, pair, share),
+                  mx_gemm_of(false, mxg::kGatedBackward, pair, share), mx_gemm_of(true, mxg::kPlain, pair, share)})
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mxg::kSmemBudget);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mx4::a4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mx4::kSmemBytes);
     for (int ctas = 1; ctas <= mxg::kMaxCluster && e == cudaSuccess; ++ctas) {
@@ -80,7 +88,7 @@ int mx_device(DeviceInfo **d) {
         cudaLaunchAttribute cl = mx_cluster(ctas);
         cfg.attrs = &cl;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[ctas], mx_gemm_of(true, mxg::kPlain, false), &cfg);
+        e = cudaOccupancyMaxActiveClusters(&(*d)->mx_clusters[ctas], mx_gemm_of(true, mxg::kPlain, false, mxg::kNone), &cfg);
     }
     if (e != cudaSuccess) return cuda_fail(e);
     (*d)->mx_ready = true;
@@ -123,15 +131,18 @@ mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilo
 }
 
 // CTAs work in pairs on 256 rows, or alone on 128 where there are no more (64 rows x 9728 x 2560: 14.2 us
-// alone, 16.5 in pairs).  The outputs of a tile (bn) and how many pairs or CTAs share its contraction
+// alone, 16.5 in pairs).  The outputs of a tile (bn) and how many pairs or CTAs share a tile's contraction
 // (splits) are those of the least estimated time in SM cycles: a stage takes its eight MMAs (half a
 // cycle an output, and about 52 cycles at least) or the expanding of a CTA's codes (measured: 450
-// cycles and 3.25 an output); a persistent grid runs rounds of tiles, a split one has to fit the
-// device at once and pays for the exchange of sums.  Any number of splits up to a cluster of eight (64
-// rows, gradients of 2 x 9728 x 2560: 50.9 us, 52.8 with powers of two alone).
+// cycles and 3.25 an output); a persistent grid runs rounds of tiles, and the tiles that do not fill a
+// round may be shared, one a cluster of up to eight CTAs, if they then fit the device at once, for the
+// price of an exchange of sums.  Backward, 2048 x 9728 x 2560: 80.8 us in two rounds of 192 outputs, the
+// second half empty, 72.8 in one of 256 and a shared one; gated block, 40 rows x 2 x 9728 x 2560: 23.2 and
+// 21.5; 64 rows, backward of 19456 x 2560, shared by six: 25.6, by four at most: 27.5.
 struct MxShape {
     bool pair = true;
     int bn = 0, splits = 1;
+    int64_t full = 0, clusters = 0;   // tiles computed by one pair or CTA each; clusters of the grid
 };
 MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragged, const DeviceInfo *d) {
     const int64_t steps = (C + mxg::kStep - 1) / mxg::kStep;
@@ -146,12 +157,16 @@ MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragge
         const int64_t stage = std::max(8 * std::max(bn / 2, 52) + 60, 450 + 13 * bn / (4 * ctas));
         for (int S = 1; ctas * S <= mxg::kMaxCluster; ++S) {
             const int64_t room = std::max<int64_t>(1, std::min<int64_t>(d->mx_clusters[ctas * S], d->sms / (ctas * S)));
-            if (S > 1 && (tiles > room || steps < 2 * S || !mxg::sums_fit(bn, ctas, S))) continue;
-            const int64_t rounds = S > 1 ? 1 : (tiles + room - 1) / room;
-            const int64_t c = rounds * (((steps + S - 1) / S) * stage + 500) + (S > 1 ? 3000 + 1000 * S : 0);
+            const int64_t full = S > 1 ? tiles / (room * S) * (room * S) : tiles, rest = tiles - full;
+            if (S > 1 && (rest == 0 || rest > room || steps < 2 * S || !mxg::sums_fit(bn, ctas, S))) continue;
+            const int64_t rounds = (full + room * S - 1) / (room * S);
+            const int64_t c = rounds * (steps * stage + 500) +
+                              (S > 1 ? (steps + S - 1) / S * stage + 500 + 3000 + 1000 * S : 0);
             if (!best.bn || c <= cost) {
                 best.bn = bn;
                 best.splits = S;
+                best.full = full;
+                best.clusters = full ? std::min(room, tiles) : rest;
                 cost = c;
             }
         }
@@ -171,6 +186,7 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     p.ks = static_cast<int>(K / mx::kBlock);
     p.bn = shape.bn;
     p.splits = shape.splits;
+    p.full = static_cast<int>(shape.full);
     const int ctas = shape.pair ? 2 : 1;
     const int64_t tm = (M + ctas * mxg::kRows - 1) / (ctas * mxg::kRows), tiles = tm * ((J + p.bn - 1) / p.bn);
     if (tiles >= kSizeLimit) return W4A16_ERR_UNSUPPORTED;
@@ -201,9 +217,9 @@ int mx_gemm(DeviceInfo *d, const void *a, const uint32_t *wq, const uint8_t *ws,
     rc = encode_2d(d, &tw, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, K / 8, N, K / 2, backward ? half / 8 : mxg::kStep / 8,
                    backward ? mxg::kStep : half, swz);
     if (rc) return rc;
-    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, d->mx_clusters[ctas]));
-    const dim3 grid(static_cast<unsigned>(ctas * p.splits * clusters), 1, 1);
-    return mx_launch(mx_gemm_of(backward, epilogue, shape.pair), grid, ctas * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
+    const dim3 grid(static_cast<unsigned>(ctas * p.splits * shape.clusters), 1, 1);
+    const int share = shape.splits == 1 ? mxg::kNone : (shape.full ? mxg::kLast : mxg::kAll);
+    return mx_launch(mx_gemm_of(backward, epilogue, shape.pair, share), grid, ctas * p.splits, mxg::kThreads, smem, stream, tx, tw, p);
 }
 
 // Outputs of a CTA pair of the 4-bit product: the fewest column-rounds of the persistent grid; an MMA

@@ -14,9 +14,9 @@
 //      [128 n][64 outputs] per group of 64 outputs, MN-major: the transposition is the descriptor's.
 // Two accumulators of 256 columns fill tensor memory: the epilogue of a tile runs under the next
 // tile's main loop.  The grid is persistent; the host picks BN for the fewest column-rounds (see
-// mx_entry.cuh).  Where the tiles leave SMs idle, S pairs (or CTAs) share a tile, a cluster of up to
-// eight CTAs, each a run of the stages; their partial sums meet in shared memory over the cluster, added
-// in split order.
+// mx_entry.cuh).  Tiles that leave SMs idle, all of them or those after the last whole round, are shared: S
+// pairs (or CTAs) of a cluster of up to eight CTAs take a run of a tile's stages each, and their partial sums
+// meet in shared memory over the cluster, added in split order.
 //
 // Roles (768 threads): warp 1 MMA issue (leader) and tensor memory, warps 0, 2-7 and 21 epilogue,
 // twelve of warps 8-23 expand codes in three teams, and beside warp 1 on its scheduler one warp that
@@ -27,12 +27,12 @@
 // waiter is a whole ring behind what it waits for: a team's next stage is in the same slot, so it has
 // waited for this one's MMAs, and the parities never alias.
 //
-// Bound, forward, 2048 x 9728 x 2560: 73 us (1.40 PFLOP/s; the tensor pipe is active 72 % of the time, the
-// integer pipe 43 %, issue slots 47 %, DRAM 4 %).  What is left is the time between two stages' MMAs: with
+// Bound, forward, 2048 x 9728 x 2560: 71.2 us (1.43 PFLOP/s; the tensor pipe is active 73 % of the time, the
+// integer pipe 44 %, issue slots 48 %, DRAM 4 %).  What is left is the time between two stages' MMAs: with
 // stages of K = 64, whose MMAs take less time than the instructions around a stage's waits do in a crowded
-// SM, the same product took 84 us.  Backward, 2048 x 9728 x 2560: 86 us, 112 tiles of 192 outputs on 74
-// pairs, so a third of the last round's pairs have none.  Few rows (33 - 128 x 9728 x 2560): 14.3 us,
-// two rounds of tiles on single CTAs, a stage as long as its codes take to expand.
+// SM, the same product took 84 us.  Backward, 2048 x 9728 x 2560: 72.8 us (1.40 PFLOP/s), of which the shared
+// last tiles save 8.  Few rows (33 - 128 x 9728 x 2560): 13.3 us: a stage is as long as its codes take to
+// expand, three at a time, each a chain of waits.
 #pragma once
 
 #include "mx.cuh"
@@ -195,10 +195,11 @@ struct Params {
     int ks;                   // scale bytes of a row of W (K / 32)
     int bn;                   // outputs of a pair
     int tiles_m, tiles;
+    int full;                 // the first tiles, which one pair (or CTA) computes alone (kLast)
     int b_bytes, w_bytes;     // B tile and codes of a CTA and stage
     int w_pitch;              // bytes of a codes tile row
     int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
-    int splits;               // pairs that share a tile (the grid then has one cluster a tile)
+    int splits;               // pairs that share each of the others (a cluster of them)
 };
 
 struct Ring {
@@ -289,7 +290,11 @@ __device__ __forceinline__ void st_dsmem_v4(uint32_t cluster_addr, uint4 v) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <bool BACKWARD, int EPILOGUE, bool PAIR>
+// Which tiles the pairs (or CTAs) of a cluster share.  (Kernels of their own: with the others' conditions
+// in it, each was 1 to 4 % slower.)
+enum Share { kNone = 0, kLast = 1, kAll = 2 };
+
+template <bool BACKWARD, int EPILOGUE, bool PAIR, int SHARE>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -307,12 +312,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rank = PAIR ? cluster_rank & 1u : 0u, lead = cluster_rank - rank;
     const bool leader = rank == 0;
     const int all_steps = (p.C + kStep - 1) / kStep, split = static_cast<int>(cluster_rank) / kCtas;
-    const int step0 = static_cast<int>(static_cast<long long>(split) * all_steps / p.splits);
-    const int steps = static_cast<int>(static_cast<long long>(split + 1) * all_steps / p.splits) - step0;
     const int half = p.bn / kCtas;                   // outputs that this CTA expands
     constexpr int kTileRows = kCtas * kRows;
-    // tiles of this pair (or CTA): first, first + pairs, ... (one tile with splits)
-    const int pairs = static_cast<int>(gridDim.x) / (kCtas * p.splits), first = static_cast<int>(blockIdx.x) / (kCtas * p.splits);
+    // Work of this pair (or CTA): tiles first, first + pairs, ... of those computed alone, all of their
+    // stages, then this split's stages of the cluster's shared tile, if it has one.
+    const int pairs = static_cast<int>(gridDim.x) / kCtas, first = static_cast<int>(blockIdx.x) / kCtas;
+    constexpr bool SHARED = SHARE != kNone;
+    const int full = SHARE == kNone ? p.tiles : (SHARE == kAll ? 0 : p.full);
+    const int shared_tile = SHARED ? full + static_cast<int>(blockIdx.x) / (kCtas * p.splits) : p.tiles;
+    struct Work {
+        int tile, step0, steps;
+    };
+    const auto work = [&](int t, Work &w) {
+        if (SHARE != kAll && t < full) {
+            w = {t, 0, all_steps};
+            return true;
+        }
+        if constexpr (!SHARED) return false;
+        if (t >= full + pairs || shared_tile >= p.tiles) return false;
+        w.tile = shared_tile;
+        w.step0 = static_cast<int>(static_cast<long long>(split) * all_steps / p.splits);
+        w.steps = static_cast<int>(static_cast<long long>(split + 1) * all_steps / p.splits) - w.step0;
+        return true;
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -355,18 +377,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring st;
         long long issued = 0;
         bool ok = true;
-        for (int t = first; t < p.tiles && ok; t += pairs) {
-            const int row = (t % p.tiles_m) * kTileRows + static_cast<int>(rank) * kRows;
-            for (int i = 0; i < steps; ++i) {
+        Work w;
+        for (int t = first; ok && work(t, w); t += pairs) {
+            const int row = (w.tile % p.tiles_m) * kTileRows + static_cast<int>(rank) * kRows;
+            for (int i = w.step0; i < w.step0 + w.steps; ++i) {
                 if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
                 if (leader) mbar_arrive_expect_tx(&ready[st.slot], kCtas * kABytes);   // both CTAs' rows
                 uint8_t *dst = sa + st.slot * kABytes;
                 if constexpr (PAIR) {
-                    tma_load_2d_pair(dst, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep, row);
-                    tma_load_2d_pair(dst + kABytes / 2, &tm_x, ready_l + 8 * st.slot, (step0 + i) * kStep + 64, row);
+                    tma_load_2d_pair(dst, &tm_x, ready_l + 8 * st.slot, i * kStep, row);
+                    tma_load_2d_pair(dst + kABytes / 2, &tm_x, ready_l + 8 * st.slot, i * kStep + 64, row);
                 } else {
-                    tma_load_2d(dst, &tm_x, &ready[st.slot], (step0 + i) * kStep, row);
-                    tma_load_2d(dst + kABytes / 2, &tm_x, &ready[st.slot], (step0 + i) * kStep + 64, row);
+                    tma_load_2d(dst, &tm_x, &ready[st.slot], i * kStep, row);
+                    tma_load_2d(dst + kABytes / 2, &tm_x, &ready[st.slot], i * kStep + 64, row);
                 }
                 ++issued;
                 st.advance(kStages);
@@ -382,15 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring st;
         long long issued = 0;
         bool ok = true;
-        for (int t = first; t < p.tiles && ok; t += pairs) {
-            const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
-            for (int i = 0; i < steps; ++i) {
+        Work w;
+        for (int t = first; ok && work(t, w); t += pairs) {
+            const int j0 = w.tile / p.tiles_m * p.bn + static_cast<int>(rank) * half;
+            for (int i = w.step0; i < w.step0 + w.steps; ++i) {
                 if (issued >= kStages && !mbar_wait(&w_empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
                 mbar_arrive_expect_tx(&w_full[st.slot], p.w_bytes);
                 if constexpr (BACKWARD)
-                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], j0 / 8, (step0 + i) * kStep);
+                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], j0 / 8, i * kStep);
                 else
-                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], (step0 + i) * (kStep / 8), j0);
+                    tma_load_2d(sw + st.slot * p.w_bytes, &tm_w, &w_full[st.slot], i * (kStep / 8), j0);
                 ++issued;
                 st.advance(kStages);
             }
@@ -405,8 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring st;
         bool ok = true;
         pdl_wait();
-        for (int t = first; t < p.tiles && ok; t += pairs)
-            for (int i = 0; i < steps && ok; ++i) {
+        Work w;
+        for (int t = first; ok && work(t, w); t += pairs)
+            for (int i = 0; i < w.steps && ok; ++i) {
                 ok = mbar_wait(&expd[st.slot], st.phase);
                 if (ok) mbar_arrive_cluster(ready_l + 8 * st.slot);
                 st.advance(kStages);
@@ -430,12 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int done = 0;
         bool ok = true;
         pdl_wait();
-        for (int t = first; t < p.tiles && ok; t += pairs, ++done) {
+        Work w;
+        for (int t = first; ok && work(t, w); t += pairs, ++done) {
             // the accumulator's previous tile has been read
             if (done >= 2 && !mbar_wait_cluster(&acc_empty[acc.slot], acc.phase ^ 1u)) break;
             tc_fence_after();
             const uint32_t d = tmem + acc.slot * 256;
-            for (int i = 0; i < steps; ++i) {
+            for (int i = 0; i < w.steps; ++i) {
                 if (!mbar_wait_spin(&ready[st.slot], st.phase)) { ok = false; break; }
                 if (issuer) {
                     const uint64_t ad = a_desc0 + st.slot * a_hop, bd = b_desc0 + st.slot * b_hop;
@@ -483,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // The codes' slot is released once they are in registers, so that its next load is under way while
         // they are expanded (us, before / after: alone, 40 rows x 19456 x 2560 24.7 / 23.2; backward, 2048 x
-        // 9728 x 2560 82.9 / 81.4), but by forward pairs at the end (512 rows 27.1 early 27.4, 1024 39.0 /
-        // 39.7).
+        // 9728 x 2560 82.9 / 81.4), but by forward pairs at the end (512 rows 27.1, early 27.4; 1024 rows
+        // 39.0, 39.7).
         constexpr bool kEarly = BACKWARD || !PAIR;
         const int stored = BACKWARD ? p.C : p.o.J;             // rows of W
         const uint8_t *ws_end = p.ws + static_cast<long long>(stored) * p.ks;
@@ -492,13 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool filled = false, ok = true;
         int i = team;                                          // this team's next stage of the tile
         pdl_wait();
-        for (int t = first; t < p.tiles && ok; t += pairs, i -= steps) {
-            const int j0 = t / p.tiles_m * p.bn + static_cast<int>(rank) * half;
+        Work w;
+        for (int t = first; ok && work(t, w); t += pairs, i -= w.steps) {
+            const int j0 = w.tile / p.tiles_m * p.bn + static_cast<int>(rank) * half;
             // row and first block of the scale bytes of stage i
-            const auto row = [&](int i) { return BACKWARD ? (step0 + i) * kStep + r : j0 + r; };
-            const auto blk = [&](int i) { return BACKWARD ? j0 / 32 : 4 * (step0 + i); };
+            const auto row = [&](int i) { return BACKWARD ? (w.step0 + i) * kStep + r : j0 + r; };
+            const auto blk = [&](int i) { return BACKWARD ? j0 / 32 : 4 * (w.step0 + i); };
             uint2 next = load_scales(p.ws, ws_end, live && row(i) < stored, row(i), blk(i), blks, p.ks);
-            for (; i < steps; i += kTeams) {
+            for (; i < w.steps; i += kTeams) {
                 const uint32_t e = scales_of(next, row(i), blk(i), p.ks);
                 next = load_scales(p.ws, ws_end, live && row(i + kTeams) < stored, row(i + kTeams), blk(i + kTeams), blks, p.ks);
                 if (!mbar_wait(&w_full[team], phase)) { ok = false; break; }
@@ -528,51 +555,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 filled = true;
             }
         }
-    } else if (epilogue && p.splits > 1) {
-        pdl_wait();
-        mbar_wait(&acc_full[0], 0, true, tile_limit_ns(steps));
     }
 
-    const int quarter = warp & 3, chunks = p.bn / 32, S = p.splits, own = (chunks + S - 1) / S;
+    const int quarter = warp & 3, chunks = p.bn / 32, S = SHARED ? p.splits : 1, own = (chunks + S - 1) / S;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, row = quarter * 32 + lane;
-    if (S > 1) {
-        // Partial sums of a tile: 32 columns belong to split (column / 32) % S.  Every warp takes part
-        // (six for each quarter of the rows); the others' columns go to their split's shared memory as
-        // [source][own columns / 32][4 columns][row] x 16 bytes, idle once the cluster's main loops are
-        // over.
+    // Partial sums of a shared tile: 32 columns belong to split (column / 32) % S.  Every warp takes part
+    // (six for each quarter of the rows), after its other work; the others' columns go to their split's
+    // shared memory as [source][own columns / 32][4 columns][row] x 16 bytes, idle once the cluster's main
+    // loops are over.
+    const auto exchange = [&]() {
         __syncwarp();
         tc_fence_before();
         cluster_sync_all();
         tc_fence_after();
+        const uint32_t sums = tmem + lanes + (first < full ? ((full - first + pairs - 1) / pairs & 1) * 256 : 0);
         for (int c = warp >> 2; c < chunks; c += kThreads / 128) {
             const int to = c % S;
             if (to == split) continue;
             uint32_t v[32];
-            tmem_ld32(tmem + lanes + 32 * c, v);
+            tmem_ld32(sums + 32 * c, v);
             tmem_ld_wait_regs(v);
             const uint32_t base = dsmem_addr(smem_u32(smem), kCtas * to + rank) + ((split * own + c / S) * 8 * kRows + row) * 16;
 #pragma unroll
             for (int q = 0; q < 8; ++q) st_dsmem_v4(base + q * kRows * 16, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
         }
         cluster_sync_all();
-    }
+    };
+    bool to_meet = SHARED && shared_tile < p.tiles;
     if (epilogue) {
         // ---------------------------------------------------------------- epilogue
         const uint32_t stage = smem_u32(ready) + kBarBytes + (epi_set * 4 + quarter) * kStageBytes;
         pdl_wait();
         Ring acc;
-        for (int t = first; t < p.tiles; t += pairs) {
-            const long long m = static_cast<long long>(t % p.tiles_m) * kTileRows + rank * kRows + row;
-            const int j0 = t / p.tiles_m * p.bn;
-            if (S == 1 && !mbar_wait(&acc_full[acc.slot], acc.phase, true, tile_limit_ns(steps))) break;
+        Work w;
+        for (int t = first; work(t, w); t += pairs) {
+            const long long m = static_cast<long long>(w.tile % p.tiles_m) * kTileRows + rank * kRows + row;
+            const int j0 = w.tile / p.tiles_m * p.bn;
+            const bool shared = SHARE == kAll || (SHARED && t >= full);
+            if (!mbar_wait(&acc_full[acc.slot], acc.phase, true, tile_limit_ns(w.steps))) break;
+            if constexpr (SHARED) {
+                if (shared) {
+                    exchange();
+                    to_meet = false;
+                }
+            }
             tc_fence_after();
-            for (int c = split + S * epi_set; c < chunks; c += 2 * S) {
+            const int every = shared ? S : 1, own_c = shared ? split : 0;
+            for (int c = own_c + every * epi_set; c < chunks; c += 2 * every) {
                 __syncwarp();                   // the loads are collective
                 uint32_t v[32];
                 tmem_ld32(tmem + lanes + acc.slot * 256 + 32 * c, v);
                 tmem_ld_wait_regs(v);
-                for (int s = 0; s < S; ++s) {   // the other splits' sums, in their order
-                    if (s == split) continue;
+                for (int s = 0; s < every; ++s) {   // the other splits' sums, in their order
+                    if (s == own_c) continue;
                     const uint32_t from = smem_u32(smem) + ((s * own + c / S) * 8 * kRows + row) * 16;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -596,13 +631,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (EPILOGUE == kPlain && (p.o.J & 7)) write_ragged(p.o, m - lane, j, v, stage, lane);
                 else if (m < p.o.M) write_columns<EPILOGUE>(p.o, m, j, v);
             }
-            if (S > 1) break;                   // one tile a cluster
+            if (shared) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc.slot);
             acc.advance(2);
         }
     }
+    if constexpr (SHARED)
+        if (to_meet) exchange();
 
     __syncwarp();
     tc_fence_before();

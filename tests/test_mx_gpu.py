@@ -247,7 +247,9 @@ def test_gate_up_backward_against_differences():
 LARGE = [(2048, 4104, 544), (257, 19456, 96), (640, 5001, 640), (129, 333, 9728), (128, 19456, 256), (64, 4096, 2560),
          (100, 151, 8192), (1000, 10007, 512), (2047, 2056, 1312), (512, 1000, 9728), (40, 2560, 9728), (300, 9728, 160),
          (40, 1280, 4096), (40, 640, 9728), (40, 1000, 16384), (40, 2048, 16384), (300, 1600, 4096), (300, 2048, 4096),
-         (300, 4096, 2560), (40, 16384, 992), (64, 9728, 640)]
+         (300, 4096, 2560), (40, 16384, 992), (64, 9728, 640),
+         # whole rounds of tiles, then shared ones
+         (64, 19456, 2560), (2048, 19456, 2560), (300, 2560, 9728), (64, 2560, 19456), (2048, 9728, 2560)]
 
 
 def whole_on_gpu(rng, rows, k):
@@ -280,7 +282,8 @@ def test_large_exact(M, N, K):
     assert w4.w4a16_device_status() == w4.OK
 
 
-@pytest.mark.parametrize("M,N,K", [(2048, 2056, 544), (509, 9728, 256), (128, 9728, 256), (64, 1000, 2560), (17, 4864, 96)])
+@pytest.mark.parametrize("M,N,K", [(2048, 2056, 544), (509, 9728, 256), (128, 9728, 256), (64, 1000, 2560), (17, 4864, 96),
+                                   (64, 9728, 2560), (1024, 9728, 2560)])
 def test_large_gated(M, N, K):
     rng = np.random.default_rng([21, M, N, K])
     wq, s = ref.random_stored(rng, 2 * N, K, 119, 121)

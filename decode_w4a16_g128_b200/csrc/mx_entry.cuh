@@ -132,13 +132,15 @@ mxg::Output mx_output(void *out, const void *dh, int64_t M, int64_t J, int epilo
 
 // CTAs work in pairs on 256 rows, or alone on 128 where there are no more (64 rows x 9728 x 2560: 14.2 us
 // alone, 16.5 in pairs).  The outputs of a tile (bn) and how many pairs or CTAs share a tile's contraction
-// (splits) are those of the least estimated time in SM cycles: a stage takes its eight MMAs (half a
-// cycle an output, and about 52 cycles at least) or the expanding of a CTA's codes (measured: 450
-// cycles and 3.25 an output); a persistent grid runs rounds of tiles, and the tiles that do not fill a
-// round may be shared, one a cluster of up to eight CTAs, if they then fit the device at once, for the
-// price of an exchange of sums.  Backward, 2048 x 9728 x 2560: 80.8 us in two rounds of 192 outputs, the
-// second half empty, 72.8 in one of 256 and a shared one; gated block, 40 rows x 2 x 9728 x 2560: 23.2 and
-// 21.5; 64 rows, backward of 19456 x 2560, shared by six: 25.6, by four at most: 27.5.
+// (splits) are those of the least estimated time in SM cycles: a stage takes a pair 283 cycles and three an
+// output, or either as long as a CTA's codes take to expand, 450 cycles and 3.25 an output of the CTA, and a
+// pair about 40 more where a warp of the expanding has rows to spare (all measured: stages of 128, 192 and
+// 256 outputs at 2048 x 4096 x 4096 took 0.43, 0.54 and 0.68 us); a persistent grid runs rounds of tiles, and
+// the tiles that do not fill a round may be shared, one a cluster of up to eight CTAs, if they then fit the
+// device at once, for the price of an exchange of sums.  Backward, 2048 x 9728 x 2560: 80.8 us in two rounds
+// of 192 outputs, the second half empty, 72.8 in one of 256 and a shared one; gated block, 40 rows x 2 x
+// 9728 x 2560: 23.2 and 21.5; 64 rows, backward of 19456 x 2560, shared by six: 25.6, by four at most: 27.5;
+// 2048 x 4096 x 4096 by 256 outputs 49.0, by 160, which a count of MMAs alone would choose, 55.5.
 struct MxShape {
     bool pair = true;
     int bn = 0, splits = 1;
@@ -154,14 +156,15 @@ MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragge
     const int most = ctas == 1 ? 128 : (ragged ? mxg::kMaxRaggedBN : mxg::kMaxBN);
     for (int bn = 32 * ctas; bn <= most; bn += backward || ctas == 1 ? 32 * ctas : 32) {
         const int64_t tiles = tm * ((J + bn - 1) / bn);
-        const int64_t stage = std::max(8 * std::max(bn / 2, 52) + 60, 450 + 13 * bn / (4 * ctas));
+        const int half = bn / ctas;
+        const int64_t stage = best.pair ? std::max(283 + 3 * bn, 450 + 13 * half / 4) + (half % 32 ? 40 : 0) : 450 + 13 * half / 4;
         for (int S = 1; ctas * S <= mxg::kMaxCluster; ++S) {
             const int64_t room = std::max<int64_t>(1, std::min<int64_t>(d->mx_clusters[ctas * S], d->sms / (ctas * S)));
             const int64_t full = S > 1 ? tiles / (room * S) * (room * S) : tiles, rest = tiles - full;
             if (S > 1 && (rest == 0 || rest > room || steps < 2 * S || !mxg::sums_fit(bn, ctas, S))) continue;
             const int64_t rounds = (full + room * S - 1) / (room * S);
             const int64_t c = rounds * (steps * stage + 500) +
-                              (S > 1 ? (steps + S - 1) / S * stage + 500 + 3000 + 1000 * S : 0);
+                              (S > 1 ? (steps + S - 1) / S * stage + 3500 + 500 * S + 4 * bn * (S - 1) : 0);
             if (!best.bn || c <= cost) {
                 best.bn = bn;
                 best.splits = S;

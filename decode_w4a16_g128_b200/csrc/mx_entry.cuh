@@ -161,7 +161,7 @@ MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragge
         for (int S = 1; ctas * S <= mxg::kMaxCluster; ++S) {
             const int64_t room = std::max<int64_t>(1, std::min<int64_t>(d->mx_clusters[ctas * S], d->sms / (ctas * S)));
             const int64_t full = S > 1 ? tiles / (room * S) * (room * S) : tiles, rest = tiles - full;
-            if (S > 1 && (rest == 0 || rest > room || steps < 2 * S || !mxg::sums_fit(bn, ctas, S))) continue;
+            if (S > 1 && (d->mx_clusters[ctas * S] < 1 || rest == 0 || rest > room || steps < 2 * S || !mxg::sums_fit(bn, ctas, S))) continue;
             const int64_t rounds = (full + room * S - 1) / (room * S);
             const int64_t c = rounds * (steps * stage + 500) +
                               (S > 1 ? (steps + S - 1) / S * stage + 3500 + 500 * S + 4 * bn * (S - 1) : 0);
@@ -272,8 +272,8 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
 }
 
 // Few rows of x take the matvec: up to 16 always, up to 32 where the weight is small.  Measured, us,
-// matvec / GEMM: M = 16 N x K 9728 x 2560 11.4 / 14.3, 2560 x 9728 15.5 / 17.5; M = 32 1024 x 2560
-// 6.8 / 9.7, 4096 x 2560 8.8 / 11.1, but 2560 x 9728 26.7 / 17.4 and 19456 x 2560 38 / 26.5.
+// matvec / GEMM: M = 16 N x K 9728 x 2560 11.1 / 13.2, 2560 x 9728 15.1 / 16.5; M = 32 1024 x 2560
+// 6.7 / 9.4, 4096 x 2560 8.9 / 10.8, but 2560 x 9728 26.7 / 16.5 and 19456 x 2560 38 / 22.4.
 bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
     return M <= 16 || (M <= mxv::kMaxM && N * K <= (int64_t(1) << 24));
 }
@@ -286,13 +286,14 @@ int mx_matvec_launch(const mxv::Params &p, void *stream) {
 
 // Warps of a CTA (they share its rows' K): as many as leave every CTA resident at once, 16 (one
 // CTA an SM), 8 (two) or 4 (five).  Measured at M = 1, us, with 16 / 8 / 4 warps: N x K 2560 x 9728
-// 10.7 / 9.9 / 13.1, 4096 x 2560 5.8 / 4.0 / 5.4, 9728 x 2560 12.4 / 8.7 / 7.0.
+// 10.7 / 9.9 / 13.1, 4096 x 2560 5.8 / 3.9 / 5.4, 9728 x 2560 12.4 / 8.7 / 7.0.  Groups in flight a warp: as
+// many as there are registers for (M = 12, 8 warps: 1024 x 2560 4.4 with two, 4.0 with four).
 template <bool X4>
 int mx_matvec_8(const mxv::Params &p, const DeviceInfo *d, void *stream) {
     const int64_t blocks = (int64_t(p.N) + 15) / 16;
-    if (blocks <= d->sms) return mx_matvec_launch<1, 16, 2, 1, X4>(p, stream);
-    if (blocks <= 2 * d->sms) return mx_matvec_launch<1, 8, 2, 2, X4>(p, stream);
-    return mx_matvec_launch<1, 4, 2, 5, X4>(p, stream);
+    if (blocks <= d->sms) return mx_matvec_launch<1, 16, 4, 1, X4>(p, stream);
+    if (blocks <= 2 * d->sms) return mx_matvec_launch<1, 8, 4, 2, X4>(p, stream);
+    return mx_matvec_launch<1, 4, 4, 5, X4>(p, stream);
 }
 
 mxv::Params mx_matvec_params(const uint32_t *wq, const uint8_t *ws, void *out, int64_t M, int64_t N, int64_t K) {
@@ -313,17 +314,17 @@ int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *w
     p.gated = gated ? 1 : 0;
     if (M <= 8) return mx_matvec_8<false>(p, d, stream);
     if (M <= 16) {
-        if ((N + 15) / 16 <= 2 * d->sms) return mx_matvec_launch<2, 8, 2, 2, false>(p, stream);
-        return mx_matvec_launch<2, 4, 1, 5, false>(p, stream);
+        if ((N + 15) / 16 <= 2 * d->sms) return mx_matvec_launch<2, 8, 4, 2, false>(p, stream);
+        return mx_matvec_launch<2, 4, 2, 5, false>(p, stream);
     }
     return mx_matvec_launch<4, 8, 1, 2, false>(p, stream);
 }
 
-// The same with x in 4 bits, for up to 8 rows and small weights: past that the FP4 tensor cores are no
-// slower, as here x is expanded anew for every 16 weight rows.  Measured, us, this / FP4 tensor cores: M = 1
-// N x K 1024 x 2560 4.8 / 8.4, 4096 x 2560 6.5 / 9.0, 1024 x 16384 10.9 / 21.0, 9728 x 2560 9.8 / 10.4; M = 8
-// 4096 x 2560 7.2 / 9.0, 8192 x 2048 8.9 / 8.6; M = 16 6400 x 2560 11.8 / 9.4.
-bool mx_few_a4(int64_t M, int64_t N, int64_t K) { return M <= 8 && N * K <= (int64_t(1) << 24); }
+// The same with x in 4 bits, for up to 8 rows and all but the largest weights: past that the FP4 tensor
+// cores are faster, as here x is expanded anew for every 16 weight rows.  Measured, us, this / FP4 tensor
+// cores: N x K 1024 x 2560 M = 1 4.7 / 8.4, 4096 x 2560 M = 8 5.8 / 9.0, 9728 x 2560 M = 8 9.7 / 10.6, 2560 x
+// 9728 M = 8 13.1 / 16.6, 19456 x 2560 M = 4 14.7 / 14.8, but 9728 x 9728 M = 8 31.3 / 23.5.
+bool mx_few_a4(int64_t M, int64_t N, int64_t K) { return M <= 8 && N * K <= (int64_t(1) << 26); }
 
 int mx_matvec_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *wq, const uint8_t *ws, void *out,
                  int64_t M, int64_t N, int64_t K, void *stream) {

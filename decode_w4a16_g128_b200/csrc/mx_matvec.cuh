@@ -12,8 +12,10 @@
 // BF16 too): its blocks are expanded like W's.
 //
 // Split: a CTA owns 16 weight rows and its warps contiguous runs of the groups; the warps' sums join in
-// warp order through shared memory, so results repeat.  Loads of D groups are in flight a warp, and every
-// CTA is resident at once at a decode layer's sizes.
+// warp order through shared memory, so results repeat.  The codes of D groups are in flight a warp; x, which
+// all CTAs of an SM read, is taken from its cache when it is needed (with x fetched ahead too, there are
+// registers for two groups: 8 rows x 9728 x 2560 8.2 us, 7.6 so).  Every CTA is resident at once at a decode
+// layer's sizes.
 // Bound: one row x 9728 x 2560 (13 MB) takes 7.0 us where its bytes take 2.0: launch, first loads and the
 // join are half of it, and the expanding keeps the integer pipe 52 % busy (tensor pipe and DRAM 14 %).
 #pragma once
@@ -148,24 +150,18 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) matvec_kernel(const Params p
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nb][0][i] = acc[nb][1][i] = 0.f;
     Codes st[D];
-    Rows<NB, X4> x[NB == 1 ? D : 1];
+    Rows<NB, X4> x;
 #pragma unroll
     for (int j = 0; j < D; ++j)
-        if (ga + j < gb) {
-            load_codes(st[j], p, ga + j, row0, g, t);
-            if constexpr (NB == 1) load_rows<NB, X4>(x[j], p, ga + j, g, t);
-        }
+        if (ga + j < gb) load_codes(st[j], p, ga + j, row0, g, t);
     for (int gi = ga; gi < gb; gi += D) {
 #pragma unroll
         for (int j = 0; j < D; ++j) {
             const int group = gi + j;
             if (group >= gb) break;
-            if constexpr (NB > 1) load_rows<NB, X4>(x[0], p, group, g, t);
-            multiply<NB, X4>(st[j], x[NB == 1 ? j : 0], acc);
-            if (group + D < gb) {
-                load_codes(st[j], p, group + D, row0, g, t);
-                if constexpr (NB == 1) load_rows<NB, X4>(x[j], p, group + D, g, t);
-            }
+            load_rows<NB, X4>(x, p, group, g, t);
+            multiply<NB, X4>(st[j], x, acc);
+            if (group + D < gb) load_codes(st[j], p, group + D, row0, g, t);
         }
     }
 #pragma unroll

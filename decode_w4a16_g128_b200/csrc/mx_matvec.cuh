@@ -17,7 +17,7 @@
 // registers for two groups: 8 rows x 9728 x 2560 8.2 us, 7.6 so).  Every CTA is resident at once at a decode
 // layer's sizes.
 // Bound: one row x 9728 x 2560 (13 MB) takes 7.0 us where its bytes take 2.0: launch, first loads and the
-// join are half of it, and the expanding keeps the integer pipe 52 % busy (tensor pipe and DRAM 14 %).
+// join are half of it, and the expanding keeps the integer pipe half busy (tensor pipe 11 %, DRAM 14 %).
 #pragma once
 
 #include "mx.cuh"

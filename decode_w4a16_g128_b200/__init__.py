@@ -298,12 +298,13 @@ def w4a16_quantize(w, wq=None, scales=None, biases=None, stream=None):
 MX_BLOCK = 32
 
 _torch = None            # torch and what the checks compare with, bound by the first call
-_bf16 = _f32 = _i32 = _u32 = _u8 = None
+_Tensor = _bf16 = _f32 = _i32 = _u32 = _u8 = None
 
 
 def _mx_setup():
-    global _torch, _bf16, _f32, _i32, _u32, _u8
+    global _torch, _Tensor, _bf16, _f32, _i32, _u32, _u8
     import torch
+    _Tensor = torch.Tensor
     _bf16, _f32, _i32, _u32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint32, torch.uint8
     _torch = torch
 
@@ -314,8 +315,8 @@ def _mx_ok(t, dtype, rows, cols, device):
 
 
 def _mx_refuse(name, t, dtypes, shape, device=None):
-    """Why a tensor is not what its function needs."""
-    if not isinstance(t, _torch.Tensor):
+    """Raises if a tensor is not what its function needs, and says why."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
@@ -327,41 +328,48 @@ def _mx_refuse(name, t, dtypes, shape, device=None):
         raise ValueError(f"{name} is on {t.device}, not on cuda:{device} like the first argument")
 
 
-def _mx_rows(name, t, *dtypes):
-    """Rows, columns and device of the first argument (bfloat16 unless types are given)."""
+def _mx_rows(name, t):
+    """Rows, columns and device of the first argument, bfloat16."""
     if _torch is None:
         _mx_setup()
-    if not dtypes:
-        dtypes = (_bf16,)
-    if not (isinstance(t, _torch.Tensor) and t.dtype in dtypes and t.is_cuda and t.dim() == 2 and t.is_contiguous()):
-        _mx_refuse(name, t, dtypes, None)
-    rows, cols = t.shape
-    return rows, cols, t.get_device()
+    if isinstance(t, _Tensor) and t.dtype is _bf16 and t.is_contiguous():
+        shape, device = t.shape, t.get_device()
+        if len(shape) == 2 and device >= 0:
+            return shape[0], shape[1], device
+    _mx_refuse(name, t, (_bf16,), None)
 
 
-def _mx_weights(wq, scales, K, device, names=("wq", "scales")):
-    """Rows N of stored codes [N, K/8] with their scales [N, K/32]."""
+def _mx_stored(codes, scales, K, device, names=("wq", "scales")):
+    """Rows N and device of stored codes [N, K/8] with their scales [N, K/32]; K and the device
+    (by index) are those of the first argument, or None where that is `codes`."""
+    if _torch is None:
+        _mx_setup()
+    if isinstance(codes, _Tensor) and (codes.dtype is _i32 or codes.dtype is _u32) and codes.is_contiguous():
+        shape, on = codes.shape, codes.get_device()
+        if len(shape) == 2 and on >= 0:
+            N, words = shape
+            if (K is None or words * 8 == K and on == device) and words % 4 == 0 and isinstance(scales, _Tensor) and (
+                    _mx_ok(scales, _u8, N, words // 4, on)):
+                return N, words * 8, on
+    if K is None:
+        _mx_refuse(names[0], codes, (_i32, _u32), None)
+        K, device = codes.shape[1] * 8, codes.get_device()
     if K % MX_BLOCK:
         raise W4A16Error(ERR_UNSUPPORTED, f"rows of {K} values: K must be a multiple of {MX_BLOCK}")
-    if not isinstance(wq, _torch.Tensor) or wq.dim() != 2:
-        _mx_refuse(names[0], wq, (_i32, _u32), None)
-    N = wq.shape[0]
-    if not (_mx_ok(wq, _i32, N, K // 8, device) or _mx_ok(wq, _u32, N, K // 8, device)):
-        _mx_refuse(names[0], wq, (_i32, _u32), (N, K // 8), device)
-    if not (isinstance(scales, _torch.Tensor) and _mx_ok(scales, _u8, N, K // MX_BLOCK, device)):
-        _mx_refuse(names[1], scales, (_u8,), (N, K // MX_BLOCK), device)
-    return N
+    N = codes.shape[0] if isinstance(codes, _Tensor) and codes.dim() == 2 else 0
+    _mx_refuse(names[0], codes, (_i32, _u32), (N, K // 8), device)
+    _mx_refuse(names[1], scales, (_u8,), (N, K // MX_BLOCK), device)
 
 
 def _mx_out(name, t, like, dtype, rows, cols, device, stream):
     """A given output, checked, or a new one; new memory that another stream than its own will
     write is recorded on that stream."""
     if t is None:
-        t = like.new_empty((rows, cols), dtype=dtype)
+        t = like.new_empty((rows, cols)) if dtype is like.dtype else like.new_empty((rows, cols), dtype=dtype)
         if stream is not None:
             t.record_stream(stream if hasattr(stream, "cuda_stream")
                             else _torch.cuda.ExternalStream(int(stream), device))
-    elif not (isinstance(t, _torch.Tensor) and (_mx_ok(t, dtype, rows, cols, device) or (
+    elif not (isinstance(t, _Tensor) and (_mx_ok(t, dtype, rows, cols, device) or (
             dtype is _i32 and _mx_ok(t, _u32, rows, cols, device)))):
         _mx_refuse(name, t, (_i32, _u32) if dtype is _i32 else (dtype,), (rows, cols), device)
     return t
@@ -387,7 +395,10 @@ def w4a16_mx_quantize(w, wq=None, scales=None, stream=None):
     MXFP4: returns (wq int32 [N, K/8], scales uint8 [N, K/32])."""
     if _torch is None:
         _mx_setup()
-    N, K, device = _mx_rows("w", w, _f32, _bf16)
+    if not (isinstance(w, _Tensor) and (w.dtype is _bf16 or w.dtype is _f32) and w.is_contiguous() and w.dim() == 2
+            and w.is_cuda):
+        _mx_refuse("w", w, (_f32, _bf16), None)
+    (N, K), device = w.shape, w.get_device()
     if K % MX_BLOCK:
         raise W4A16Error(ERR_UNSUPPORTED, "w4a16_mx_quantize")
     wq = _mx_out("wq", wq, w, _i32, N, K // 8, device, stream)
@@ -399,11 +410,7 @@ def w4a16_mx_quantize(w, wq=None, scales=None, stream=None):
 
 def w4a16_mx_dequantize(wq, scales, w=None, dtype=None, stream=None):
     """The values of stored codes [N, K], bfloat16 (default) or float32; both hold them exactly."""
-    if _torch is None:
-        _mx_setup()
-    N, words, device = _mx_rows("wq", wq, _i32, _u32)
-    K = words * 8
-    _mx_weights(wq, scales, K, device)
+    N, K, device = _mx_stored(wq, scales, None, None)
     if dtype is None:
         dtype = _bf16 if w is None else w.dtype
     if dtype is not _f32 and dtype is not _bf16:
@@ -417,7 +424,7 @@ def w4a16_mx_dequantize(wq, scales, w=None, dtype=None, stream=None):
 def w4a16_mx_matmul(x, wq, scales, y=None, stream=None):
     """y [M, N] = x . W^T for W in MXFP4; x and y bfloat16, any M."""
     M, K, device = _mx_rows("x", x)
-    N = _mx_weights(wq, scales, K, device)
+    N = _mx_stored(wq, scales, K, device)[0]
     y = _mx_out("y", y, x, _bf16, M, N, device, stream)
     _mx_run(lib.w4a16_mx_matmul, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K)
     return y
@@ -425,12 +432,8 @@ def w4a16_mx_matmul(x, wq, scales, y=None, stream=None):
 
 def w4a16_mx_matmul_a4(xq, xscales, wq, scales, y=None, stream=None):
     """y [M, N] = X . W^T with both operands in MXFP4 (X from w4a16_mx_quantize of the activations)."""
-    if _torch is None:
-        _mx_setup()
-    M, words, device = _mx_rows("xq", xq, _i32, _u32)
-    K = words * 8
-    _mx_weights(xq, xscales, K, device, ("xq", "xscales"))
-    N = _mx_weights(wq, scales, K, device)
+    M, K, device = _mx_stored(xq, xscales, None, None, ("xq", "xscales"))
+    N = _mx_stored(wq, scales, K, device)[0]
     y = _mx_out("y", y, xq, _bf16, M, N, device, stream)
     _mx_run(lib.w4a16_mx_matmul_a4, device, stream, xq.data_ptr(), xscales.data_ptr(), wq.data_ptr(), scales.data_ptr(),
             y.data_ptr(), M, N, K)
@@ -441,7 +444,7 @@ def w4a16_mx_gate_up(x, wq, scales, h=None, stream=None):
     """Gated block, any M: h [M, N2] = bf16(silu(x . gate^T) * (x . up^T)), the two layers' rows
     interleaved in blocks of 8 (interleave_gate_up) in wq and scales (2 N2 rows)."""
     M, K, device = _mx_rows("x", x)
-    N = _mx_weights(wq, scales, K, device)
+    N = _mx_stored(wq, scales, K, device)[0]
     if N % 16:
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
     h = _mx_out("h", h, x, _bf16, M, N // 2, device, stream)
@@ -452,11 +455,11 @@ def w4a16_mx_gate_up(x, wq, scales, h=None, stream=None):
 def w4a16_mx_matmul_backward(dy, wq, scales, dx=None, stream=None):
     """The input's gradient of w4a16_mx_matmul: dx [M, K] = dy [M, N] . W; N a multiple of 8."""
     M, N, device = _mx_rows("dy", dy)
-    if not isinstance(wq, _torch.Tensor) or wq.dim() != 2:
-        _mx_refuse("wq", wq, (_i32, _u32), None)
-    K = wq.shape[1] * 8
-    if _mx_weights(wq, scales, K, device) != N:
-        raise ValueError(f"dy has {N} columns, W {wq.shape[0]} rows")
+    rows, K, on = _mx_stored(wq, scales, None, None)
+    if on != device:
+        _mx_refuse("wq", wq, (_i32, _u32), None, device)
+    if rows != N:
+        raise ValueError(f"dy has {N} columns, W {rows} rows")
     dx = _mx_out("dx", dx, dy, _bf16, M, K, device, stream)
     _mx_run(lib.w4a16_mx_matmul_backward, device, stream, dy.data_ptr(), wq.data_ptr(), scales.data_ptr(), dx.data_ptr(),
             M, N, K)
@@ -467,10 +470,10 @@ def w4a16_mx_gate_up_backward(x, wq, scales, dh, dx=None, dgu=None, stream=None)
     """Backward pass of w4a16_mx_gate_up from x and dh [M, N2]: returns (dx [M, K], dgu [M, 2 N2]),
     dgu the gradients of both projections' outputs with columns interleaved like the rows of W."""
     M, K, device = _mx_rows("x", x)
-    N = _mx_weights(wq, scales, K, device)
+    N = _mx_stored(wq, scales, K, device)[0]
     if N % 16:
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
-    if not (isinstance(dh, _torch.Tensor) and _mx_ok(dh, _bf16, M, N // 2, device)):
+    if not (isinstance(dh, _Tensor) and _mx_ok(dh, _bf16, M, N // 2, device)):
         _mx_refuse("dh", dh, (_bf16,), (M, N // 2), device)
     dx = _mx_out("dx", dx, x, _bf16, M, K, device, stream)
     dgu = _mx_out("dgu", dgu, x, _bf16, M, N, device, stream)

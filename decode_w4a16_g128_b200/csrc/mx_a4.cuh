@@ -62,6 +62,7 @@ struct Params {
     const uint8_t *xs, *ws;   // scales [M, K/32], [N, K/32]
     int K, bn;
     int tiles_n, tiles;
+    int x_bytes;              // of a CTA's rows of x in a stage
 };
 
 // ------------------------------------------------------------------ PTX
@@ -254,8 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int row = row_of(t), out = out_of(t) + static_cast<int>(rank) * half;
                 for (int i = 0; i < steps; ++i) {
                     if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(&ready[st.slot], 2 * (kABytes + half * (kStep / 2)));
-                    tma_load_2d_pair(smem + st.slot * kABytes, &tm_x, ready_l + 8 * st.slot, i * (kStep / 8), row);
+                    // rows of x that there are none of are not loaded: theirs are sums that no one reads
+                    if (leader)
+                        mbar_arrive_expect_tx(&ready[st.slot], (row + kRows < p.o.M ? 2 : 1) * p.x_bytes + half * kStep);
+                    if (row < p.o.M) tma_load_2d_pair(smem + st.slot * kABytes, &tm_x, ready_l + 8 * st.slot, i * (kStep / 8), row);
                     tma_load_2d_pair(sb + st.slot * kBBytes, &tm_w, ready_l + 8 * st.slot, i * (kStep / 8), out);
                     ++issued;
                     st.advance(kStages);

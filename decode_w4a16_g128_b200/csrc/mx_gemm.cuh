@@ -197,6 +197,7 @@ struct Params {
     int tiles_m, tiles;
     int full;                 // the first tiles, which one pair (or CTA) computes alone (kLast)
     int b_bytes, w_bytes;     // B tile and codes of a CTA and stage
+    int x_bytes;              // of a CTA's rows of x in a stage: all 128, or (alone) the M there are
     int w_pitch;              // bytes of a codes tile row
     int w_swz_shift, w_swz_mask;   // its 16-byte chunks are XORed with (row >> shift) & mask
     int splits;               // pairs that share each of the others (a cluster of them)
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = (w.tile % p.tiles_m) * kTileRows + static_cast<int>(rank) * kRows;
             for (int i = w.step0; i < w.step0 + w.steps; ++i) {
                 if (issued >= kStages && !mbar_wait(&empty[st.slot], st.phase ^ 1u)) { ok = false; break; }
-                if (leader) mbar_arrive_expect_tx(&ready[st.slot], kCtas * kABytes);   // both CTAs' rows
+                if (leader) mbar_arrive_expect_tx(&ready[st.slot], kCtas * p.x_bytes);   // both CTAs' rows
                 uint8_t *dst = sa + st.slot * kABytes;
                 if constexpr (PAIR) {
                     tma_load_2d_pair(dst, &tm_x, ready_l + 8 * st.slot, i * kStep, row);

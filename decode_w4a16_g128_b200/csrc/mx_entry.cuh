@@ -158,7 +158,7 @@ MxShape mx_gemm_shape(int64_t M, int64_t J, int64_t C, bool backward, bool ragge
     best.pair = M > mxg::kRows;
     const int ctas = best.pair ? 2 : 1;
     const int64_t tm = (M + ctas * mxg::kRows - 1) / (ctas * mxg::kRows);
-    const int most = ctas == 1 ? 128 : (ragged ? mxg::kMaxRaggedBN : mxg::kMaxBN);
+    const int most = (ragged ? mxg::kMaxRaggedBN : mxg::kMaxBN) * ctas / 2;
     for (int bn = 32 * ctas; bn <= most; bn += backward || ctas == 1 ? 32 * ctas : 32) {
         const int64_t tiles = tm * ((J + bn - 1) / bn);
         const int half = bn / ctas;

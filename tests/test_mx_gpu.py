@@ -249,7 +249,9 @@ LARGE = [(2048, 4104, 544), (257, 19456, 96), (640, 5001, 640), (129, 333, 9728)
          (40, 1280, 4096), (40, 640, 9728), (40, 1000, 16384), (40, 2048, 16384), (300, 1600, 4096), (300, 2048, 4096),
          (300, 4096, 2560), (40, 16384, 992), (64, 9728, 640),
          # whole rounds of tiles, then shared ones
-         (64, 19456, 2560), (2048, 19456, 2560), (300, 2560, 9728), (64, 2560, 19456), (2048, 9728, 2560)]
+         (64, 19456, 2560), (2048, 19456, 2560), (300, 2560, 9728), (64, 2560, 19456), (2048, 9728, 2560),
+         # the widest tiles of outputs that start at odd addresses, alone and in pairs
+         (40, 2047, 16384), (90, 18001, 2048), (2000, 4001, 2048)]
 
 
 def whole_on_gpu(rng, rows, k):

@@ -233,11 +233,15 @@ __global__ void __launch_bounds__(kQThreads) dequantize_kernel(const uint2 *wq, 
 
 // ------------------------------------------------------------------ the gated block's scalar parts
 
-// silu(g) u and its derivatives, from FP32 sums: silu(g) = g s, s = 1 / (1 + e^-g).  The fast
-// exponential and division: together off by at most (6 + 1.2 |g|) 2^-23 of s, a thousandth of the
-// results' BF16 step at the far end of the exponential's range (with the exact functions an epilogue
-// of these outputs took longer than its tile's products).  A large negative g gives s = 0.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// silu(g) u and its derivatives, from FP32 sums: silu(g) = g s, s = 1 / (1 + e^-g), for negative g as
+// e^g / (1 + e^g), so that nothing overflows and small s stay.  The fast exponential and division: together
+// off by at most (6 + 1.2 |g|) 2^-23 of s, a thousandth of the results' BF16 step at the far end of the
+// exponential's range (with the exact functions an epilogue of these outputs took longer than its tile's
+// products).  Below 2^-126 s may count as 0.
+__device__ __forceinline__ float sigmoid(float g) {
+    const float t = __expf(-fabsf(g));
+    return __fdividef(g < 0.f ? t : 1.f, 1.f + t);
+}
 __device__ __forceinline__ float gated(float g, float u) { return g * sigmoid(g) * u; }
 __device__ __forceinline__ void gated_backward(float g, float u, float dh, float &dg, float &du) {
     const float s = sigmoid(g);

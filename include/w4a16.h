@@ -364,7 +364,8 @@ int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_
 /*
  * Gated feed-forward block: h [M, N2] = bf16(silu(g) * u), g = x . Wg^T, u = x . Wu^T in FP32.  The
  * rows of Wg and Wu are interleaved in blocks of 8 as in w4a16_gate_up: wq [2 N2, K/8], scales
- * [2 N2, K/32].  N2 % 8 == 0 (else W4A16_ERR_UNSUPPORTED); any M.
+ * [2 N2, K/32].  N2 % 8 == 0 (else W4A16_ERR_UNSUPPORTED); any M.  The sigmoid is evaluated in FP32;
+ * below 2^-126 (g < -87) it may count as 0, here and in the gradients.
  */
 int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, void *h, int64_t M, int64_t N2,
                      int64_t K, void *stream);

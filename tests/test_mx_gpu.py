@@ -544,6 +544,25 @@ def test_refusals_on_the_device():
     assert e.value.status == w4.ERR_MISALIGNED
 
 
+@pytest.mark.parametrize("M", [4, 40])
+def test_gate_up_far_out(M):
+    """Gates from -200 to 200: no overflow, and only sigmoids below 2^-126 may be lost."""
+    K, N = 32, 64                                  # w = 1 at one k of a row: g and u are values of x
+    codes = np.zeros((2 * N, K), np.uint32)
+    gate = (np.arange(2 * N) // 8) % 2 == 0
+    codes[gate, 3] = codes[~gate, 17] = 2
+    wq, s = ref.pack(codes), np.full((2 * N, 1), 127, np.uint8)
+    x = np.zeros((M, K))
+    x[:, 3] = ref.bf16(np.linspace(-200, 200, M) if M > 4 else np.array([-200.0, -88.5, -80.0, 100.0]))
+    x[:, 17] = 3.0
+    w, dh = ref.values(wq, s), ref.bf16(np.ones((M, N)))
+    h, tol = ref.gate_up(x, w)
+    lost = 2.0 ** -126 * 3 * (1 + np.abs(x[:, 3:4]))       # |s| < 2^-126 times |u| and the larger factors of it
+    near(host(w4.w4a16_mx_gate_up(dev_bf16(x), *dev(wq, s))), h, tol + lost)
+    dgu, tol = ref.gate_up_backward(x, w, dh)
+    near(host(w4.w4a16_mx_gate_up_backward(dev_bf16(x), *dev(wq, s), dev_bf16(dh))[1]), dgu, tol + lost)
+
+
 def spread(picked, at, k, stored):
     """Rows of k values that are zeros but for codes picked [rows, len(at)] at columns `at`."""
     rows, words = picked.shape[0], [i // 8 for i in at]

@@ -4,6 +4,11 @@
 // 2^(e - 127); 255 marks a block that is not a number) and 32 codes of 4 bits: sign, two exponent
 // bits, one mantissa bit, standing for 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.  Eight codes a
 // word, the lowest k in the lowest bits, so codes are uint32 [rows, K/8], scales uint8 [rows, K/32].
+//
+// Codes and scales may come from the quantiser, which releases the next kernel at once: that kernel begins
+// before they are written, perhaps on an SM whose cache still holds older ones.  So these kernels read all
+// of their inputs behind pdl_wait(), by plain loads or TMA; the non-coherent path would need data that do
+// not change from a kernel's beginning on.
 #pragma once
 
 #include "ptx.cuh"

@@ -117,7 +117,7 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ uint4 scale_chunk(const uint8_t *at, const uint8_t *end) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     for (int i = 0; i < 16; ++i)
-        if (at + i < end) w[i >> 2] |= static_cast<uint32_t>(__ldg(at + i)) << (8 * (i & 3));
+        if (at + i < end) w[i >> 2] |= ldg_u8(at + i) << (8 * (i & 3));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -152,7 +152,7 @@ __device__ __forceinline__ void load_chunk_if(bool p, const uint8_t *at, uint4 &
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %5, 0;\n\t"
-        "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
         : "l"(at), "r"(p ? 1u : 0u));
 }

@@ -225,10 +225,10 @@ __device__ __forceinline__ unsigned long long tile_limit_ns(int steps) {
 // array starts on a 16-byte boundary), kept as loaded and looked at a stage later, since a look here
 // would wait for the load.  The array's last word may be cut off: it is read by bytes then.
 __device__ __forceinline__ uint32_t scale_word(const uint8_t *at, const uint8_t *end) {
-    if (at + 4 <= end) return __ldg(reinterpret_cast<const uint32_t *>(at));
+    if (at + 4 <= end) return ldg_u32(at);
     uint32_t v = 0;
     for (int i = 0; i < 3; ++i)
-        if (at + i < end) v |= static_cast<uint32_t>(__ldg(at + i)) << (8 * i);
+        if (at + i < end) v |= ldg_u8(at + i) << (8 * i);
     return v;
 }
 __device__ __forceinline__ uint32_t scale_offset(int row, int blk, int ks) {

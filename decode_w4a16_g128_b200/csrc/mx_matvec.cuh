@@ -62,8 +62,8 @@ __device__ __forceinline__ void load_codes(Codes &st, const Params &p, int group
         st.c[h] = make_uint4(0u, 0u, 0u, 0u);
         st.e[h] = 127u;
         if (live) {
-            st.c[h] = ldg_nc_v4(p.wq + 4 * at);
-            st.e[h] = __ldg(p.ws + at);
+            st.c[h] = ldg_v4(p.wq + 4 * at);
+            st.e[h] = ldg_u8(p.ws + at);
         }
     }
 }
@@ -84,7 +84,7 @@ __device__ __forceinline__ void load_rows(Rows<NB, X4> &st, const Params &p, int
         const long long at = static_cast<long long>(live ? m : 0) * ks + (live ? blk : 0);
         if constexpr (X4) {
             st.v[nb][0] = live ? ldg_v4(p.xq + 4 * at) : make_uint4(0u, 0u, 0u, 0u);
-            st.e[nb] = live ? *(p.xs + at) : 127u;
+            st.e[nb] = live ? ldg_u8(p.xs + at) : 127u;
         } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) st.v[nb][q] = live ? ldg_v4(p.x + mx::kBlock * at + 8 * q) : make_uint4(0u, 0u, 0u, 0u);

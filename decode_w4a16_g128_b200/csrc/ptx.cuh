@@ -485,7 +485,8 @@ __device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.
 template <uint32_t kRegs>
 __device__ __forceinline__ void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-// 128-bit read-only global load (through the non-coherent path; data not written during the kernel).
+// 128-bit read-only global load (through the non-coherent path; data not written during the kernel,
+// which under programmatic dependent launch begins before the preceding one has ended).
 __device__ __forceinline__ uint4 ldg_nc_v4(const void *p) {
     uint4 v;
     asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -546,6 +547,17 @@ __device__ __forceinline__ uint4 ldg_v4(const void *p) {
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+// The same for 4 bytes, and for one.
+__device__ __forceinline__ uint32_t ldg_u32(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ldg_u8(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 

@@ -1,0 +1,25 @@
+"""MXFP4 kernels begin before the preceding kernel of the stream has ended, so what that one writes
+must not be read through the non-coherent path (its data may not change during a kernel, and a cache
+line from before the wait would be stale): a look at the sources, on the CPU."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "decode_w4a16_g128_b200", "csrc")
+FILES = sorted(glob.glob(os.path.join(CSRC, "mx*.cuh")))
+
+
+def code(path):
+    return re.sub(r"//[^\n]*", "", open(path).read())
+
+
+@pytest.mark.parametrize("path", FILES, ids=os.path.basename)
+def test_no_load_through_the_non_coherent_path(path):
+    found = re.findall(r"__ldg\b|ldg_nc\w*|\.global\.nc\b|__restrict__", code(path))
+    assert not found, found
+
+
+def test_the_files_are_there():
+    assert len(FILES) == 5

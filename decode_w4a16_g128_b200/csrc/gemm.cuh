@@ -154,7 +154,7 @@ struct Params {
 // p0 = bf16(X), p1 = bf16(X - p0), p2 = X - p0 - p1 (exact in BF16).
 // Bc[n, 6g + j] = b[n,g], Bc[n, 6g + 3 + j] = -16 s[n,g] (one thread per (n, g)).
 // The last group of a row also writes the zero padding 6G .. Kx-1.
-__global__ void __launch_bounds__(256) prep_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ scales,
+__global__ void __launch_bounds__(256) prep_kernel(const uint16_t *x, const uint16_t *__restrict__ scales,
                                                    const uint16_t *__restrict__ biases, uint16_t *__restrict__ xs,
                                                    uint16_t *__restrict__ bc, int M, int N, int G, int Kx) {
     pdl_launch_dependents();   // the GEMM may start its prologue
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) prep_kernel(const uint16_t *__restrict__ 
         const int g = live ? static_cast<int>(u - r * G) : 0;
         float sum = 0.f;
         if (live) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x + r * K + g * 128) + l16);
+            const uint4 v = ldg_v4(reinterpret_cast<const uint4 *>(x + r * K + g * 128) + l16);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 v[8];
 #pragma unroll
                     for (int jj = 0; jj < 8; ++jj)
-                        v[jj] = row_ok ? ldg_nc_v4(bcrow + t * 16 + half * 8 + jj) : make_uint4(0, 0, 0, 0);
+                        v[jj] = row_ok ? ldg_v4(bcrow + t * 16 + half * 8 + jj) : make_uint4(0, 0, 0, 0);
                     if (g >= kABufs && !mbar_wait(&done[fs.slot], fs.phase)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll

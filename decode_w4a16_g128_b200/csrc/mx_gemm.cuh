@@ -537,8 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (src[q]) c[q] = lds128(src[q]);
                 }
                 if constexpr (kEarly) {
-                    // a vote on a word of each load waits for them; an arrival alone would overtake them
+                    // The next load may overwrite the slot once lane 0 has arrived: behind every lane's loads,
+                    // which __syncwarp orders before it (a vote alone orders no memory), and with the values
+                    // in registers, for which the vote on a word of each waits.
                     const uint32_t seen = __ballot_sync(0xFFFFFFFFu, (c[0].x ^ c[1].x ^ c[2].x ^ c[3].x) & 1u);
+                    __syncwarp();
                     if (lane == (seen == 0xFFFFFFFFu ? 31 : 0)) mbar_arrive(&w_empty[team]);
                 }
                 if (filled && !mbar_wait(&empty[team], phase ^ 1u)) { ok = false; break; }

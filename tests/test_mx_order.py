@@ -1,6 +1,8 @@
-"""MXFP4 kernels begin before the preceding kernel of the stream has ended, so what that one writes
+"""What orders the MXFP4 kernels' accesses and no result shows: looks at the sources, on the CPU.
+
+The kernels begin before the preceding kernel of the stream has ended, so what that one writes
 must not be read through the non-coherent path (its data may not change during a kernel, and a cache
-line from before the wait would be stale): a look at the sources, on the CPU."""
+line from before the wait would be stale)."""
 import glob
 import os
 import re
@@ -23,3 +25,14 @@ def test_no_load_through_the_non_coherent_path(path):
 
 def test_the_files_are_there():
     assert len(FILES) == 5
+
+
+def test_codes_are_released_behind_a_warp_barrier():
+    """A codes slot is handed back by one lane's arrival: between the warp's loads of it and that arrival
+    there has to be a barrier that orders memory, which a vote is not."""
+    text = code(os.path.join(CSRC, "mx_gemm.cuh"))
+    at = [m.start() for m in re.finditer(r"mbar_arrive\(&w_empty", text)]
+    assert len(at) == 2
+    loads = text.index("c[q] = lds128(src[q])")
+    for a in at:
+        assert "__syncwarp();" in text[loads:a]

@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (n + u >= items) break;
-                    if (n + u >= kSpans && !mbar_wait(&s_empty[sp.slot], sp.phase ^ 1u)) { ok = false; break; }
+                    if (n + u >= kSpans && !mbar_wait_warp(&s_empty[sp.slot], sp.phase ^ 1u)) { ok = false; break; }
                     put(item[u], sp.slot);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int buffer = 0;
         for (int t = t0; t < t1; ++t) {
             const int m0 = row_of(t) + quarter * 32, j0 = out_of(t);
-            if (!mbar_wait(&acc_full[acc.slot], acc.phase, true, mxg::tile_limit_ns(steps))) break;
+            if (!mbar_wait_warp(&acc_full[acc.slot], acc.phase, mxg::tile_limit_ns(steps))) break;
             tc_fence_after();
             for (int c = c0; c < c0 + half; c += 32) {
                 __syncwarp();                   // the loads are collective

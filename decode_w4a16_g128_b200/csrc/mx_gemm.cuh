@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; i < w.steps; i += kTeams) {
                 const uint32_t e = scales_of(next, row(i), blk(i), p.ks);
                 next = load_scales(p.ws, ws_end, live && row(i + kTeams) < stored, row(i + kTeams), blk(i + kTeams), blks, p.ks);
-                if (!mbar_wait(&w_full[team], phase)) { ok = false; break; }
+                if (!mbar_wait_warp(&w_full[team], phase)) { ok = false; break; }
                 uint4 c[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == (seen == 0xFFFFFFFFu ? 31 : 0)) mbar_arrive(&w_empty[team]);
                 }
-                if (filled && !mbar_wait(&empty[team], phase ^ 1u)) { ok = false; break; }
+                if (filled && !mbar_wait_warp(&empty[team], phase ^ 1u)) { ok = false; break; }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (src[q]) expand_block<BACKWARD>(c[q], dst[q], (e >> (8 * (b0 + q * share))) & 255u);
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long m = static_cast<long long>(w.tile % p.tiles_m) * kTileRows + rank * kRows + row;
             const int j0 = w.tile / p.tiles_m * p.bn;
             const bool shared = SHARE == kAll || (SHARED && t >= full);
-            if (!mbar_wait(&acc_full[acc.slot], acc.phase, true, tile_limit_ns(w.steps))) break;
+            if (!mbar_wait_warp(&acc_full[acc.slot], acc.phase, tile_limit_ns(w.steps))) break;
             if constexpr (SHARED) {
                 if (shared) {
                     exchange();

@@ -121,6 +121,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
     }
 }
 
+// mbar_wait by a whole, converged warp, with one outcome: a warp whose lanes gave up at different times
+// would go different ways, some into collective instructions that wait for the others.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity,
+                                               unsigned long long limit_ns = kWaitTimeoutNs) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, true, limit_ns));
+}
+
 // The same bounded wait without the suspend hint, for a thread whose waits are on the
 // critical path (the MMA issuer): a suspended thread was measured to resume about 60 cycles
 // later than one spinning on try_wait, and the tensor pipe idles meanwhile.

@@ -36,3 +36,17 @@ def test_codes_are_released_behind_a_warp_barrier():
     loads = text.index("c[q] = lds128(src[q])")
     for a in at:
         assert "__syncwarp();" in text[loads:a]
+
+
+@pytest.mark.parametrize("name,roles", [("mx_gemm.cuh", ("codes to BF16", "- epilogue")),
+                                        ("mx_a4.cuh", ("- scales\n", "epilogue: half of the columns"))])
+def test_a_warp_gives_up_as_one(name, roles):
+    """Warps that wait with all lanes and then take part in collective instructions must not have some of
+    them leave: their waits are those with one outcome for the warp."""
+    text = open(os.path.join(CSRC, name)).read()
+    for role in roles:
+        at = [m.start() for m in re.finditer("------ *" + role if role[0] != "-" else "-----" + role, text)]
+        assert at, role
+        section = text[at[-1]:]
+        section = section[:section.find("} else if") if "} else if" in section else len(section)]
+        assert "mbar_wait_warp(" in section and not re.search(r"\bmbar_wait(_spin|_cluster)?\(", section), role

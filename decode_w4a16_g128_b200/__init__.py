@@ -119,6 +119,38 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _side_stream(stream, device):
+    """A stream that was given as torch's, or None where it is the device's current one."""
+    import torch
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(device):
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device)
+
+
+def _empty_on(stream, device, make):
+    """A new output, make(), for work on a stream that was given.  Memory of the current stream would not
+    do: what it hands out may be memory that was freed there with work in front of it still pending, which
+    the given stream does not wait for.  So the block comes from the given stream's memory, and is not
+    reused there before the current stream, on which the caller may use it, has come past its end."""
+    import torch
+    side = _side_stream(stream, device)
+    if side is None:
+        return make()
+    with torch.cuda.stream(side):
+        t = make()
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _keep_for(stream, device, *tensors):
+    """The tensors' memory is not reused before work on a stream that was given is done with it."""
+    side = _side_stream(stream, device)
+    if side is not None:
+        for t in tensors:
+            t.record_stream(side)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
@@ -292,8 +324,11 @@ def w4a16_quantize(w, wq=None, scales=None, biases=None, stream=None):
 #
 # wq int32/uint32 [N, K/8] codes and scales uint8 [N, K/32], as in include/w4a16.h.  Tensors are
 # contiguous and on one CUDA device, which need not be the current one; outputs that are not given
-# are allocated there.  A decode loop runs these functions for every token, so each looks at what it
-# was given in one expression, and only a call that fails it goes on to find out why.
+# are allocated there.  With `stream`, the work runs on that stream, behind what is on it alone: the
+# caller orders it behind the work that makes the inputs, and uses of the outputs behind it.  New outputs
+# are then that stream's memory, and every tensor of the call may be dropped before its work is done.  A
+# decode loop runs these functions for every token, so each looks at what it was given in one expression,
+# and only a call that fails it goes on to find out why.
 
 MX_BLOCK = 32
 
@@ -362,13 +397,12 @@ def _mx_stored(codes, scales, K, device, names=("wq", "scales")):
 
 
 def _mx_out(name, t, like, dtype, rows, cols, device, stream):
-    """A given output, checked, or a new one; new memory that another stream than its own will
-    write is recorded on that stream."""
+    """A given output, checked, or a new one."""
     if t is None:
-        t = like.new_empty((rows, cols)) if dtype is like.dtype else like.new_empty((rows, cols), dtype=dtype)
-        if stream is not None:
-            t.record_stream(stream if hasattr(stream, "cuda_stream")
-                            else _torch.cuda.ExternalStream(int(stream), device))
+        if stream is None:
+            t = like.new_empty((rows, cols)) if dtype is like.dtype else like.new_empty((rows, cols), dtype=dtype)
+        else:
+            t = _empty_on(stream, device, lambda: like.new_empty((rows, cols), dtype=dtype))
     elif not (isinstance(t, _Tensor) and (_mx_ok(t, dtype, rows, cols, device) or (
             dtype is _i32 and _mx_ok(t, _u32, rows, cols, device)))):
         _mx_refuse(name, t, (_i32, _u32) if dtype is _i32 else (dtype,), (rows, cols), device)
@@ -405,6 +439,8 @@ def w4a16_mx_quantize(w, wq=None, scales=None, stream=None):
     scales = _mx_out("scales", scales, w, _u8, N, K // MX_BLOCK, device, stream)
     _mx_run(lib.w4a16_mx_quantize, device, stream, w.data_ptr(), DTYPE_F32 if w.dtype is _f32 else DTYPE_BF16,
             wq.data_ptr(), scales.data_ptr(), N, K)
+    if stream is not None:
+        _keep_for(stream, device, w, wq, scales)
     return wq, scales
 
 
@@ -418,6 +454,8 @@ def w4a16_mx_dequantize(wq, scales, w=None, dtype=None, stream=None):
     w = _mx_out("w", w, wq, dtype, N, K, device, stream)
     _mx_run(lib.w4a16_mx_dequantize, device, stream, wq.data_ptr(), scales.data_ptr(), w.data_ptr(),
             DTYPE_F32 if dtype is _f32 else DTYPE_BF16, N, K)
+    if stream is not None:
+        _keep_for(stream, device, wq, scales, w)
     return w
 
 
@@ -427,6 +465,8 @@ def w4a16_mx_matmul(x, wq, scales, y=None, stream=None):
     N = _mx_stored(wq, scales, K, device)[0]
     y = _mx_out("y", y, x, _bf16, M, N, device, stream)
     _mx_run(lib.w4a16_mx_matmul, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K)
+    if stream is not None:
+        _keep_for(stream, device, x, wq, scales, y)
     return y
 
 
@@ -437,6 +477,8 @@ def w4a16_mx_matmul_a4(xq, xscales, wq, scales, y=None, stream=None):
     y = _mx_out("y", y, xq, _bf16, M, N, device, stream)
     _mx_run(lib.w4a16_mx_matmul_a4, device, stream, xq.data_ptr(), xscales.data_ptr(), wq.data_ptr(), scales.data_ptr(),
             y.data_ptr(), M, N, K)
+    if stream is not None:
+        _keep_for(stream, device, xq, xscales, wq, scales, y)
     return y
 
 
@@ -449,6 +491,8 @@ def w4a16_mx_gate_up(x, wq, scales, h=None, stream=None):
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
     h = _mx_out("h", h, x, _bf16, M, N // 2, device, stream)
     _mx_run(lib.w4a16_mx_gate_up, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), h.data_ptr(), M, N // 2, K)
+    if stream is not None:
+        _keep_for(stream, device, x, wq, scales, h)
     return h
 
 
@@ -463,6 +507,8 @@ def w4a16_mx_matmul_backward(dy, wq, scales, dx=None, stream=None):
     dx = _mx_out("dx", dx, dy, _bf16, M, K, device, stream)
     _mx_run(lib.w4a16_mx_matmul_backward, device, stream, dy.data_ptr(), wq.data_ptr(), scales.data_ptr(), dx.data_ptr(),
             M, N, K)
+    if stream is not None:
+        _keep_for(stream, device, dy, wq, scales, dx)
     return dx
 
 
@@ -479,6 +525,8 @@ def w4a16_mx_gate_up_backward(x, wq, scales, dh, dx=None, dgu=None, stream=None)
     dgu = _mx_out("dgu", dgu, x, _bf16, M, N, device, stream)
     _mx_run(lib.w4a16_mx_gate_up_backward, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), dh.data_ptr(),
             dgu.data_ptr(), dx.data_ptr(), M, N // 2, K)
+    if stream is not None:
+        _keep_for(stream, device, x, wq, scales, dh, dx, dgu)
     return dx, dgu
 
 

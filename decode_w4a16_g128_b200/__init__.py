@@ -10,6 +10,11 @@ built (``python decode_w4a16_g128_b200/build.py``).
 Tensors: ``x`` bf16 [M, K]; ``wq`` int32/uint32 [N, K/8] (eight 4-bit codes
 per word, low nibble first); ``scales``/``biases`` bf16 [N, K/128]; the result
 ``y`` is bf16 [M, N].  All on the same CUDA device, contiguous.
+
+With ``stream``, the work runs on that stream, behind what is on it alone: the
+caller orders it behind the work that makes the inputs, and uses of the outputs
+behind it.  New outputs are then that stream's memory, and every tensor of the
+call may be dropped before its work is done.
 """
 from __future__ import annotations
 
@@ -151,6 +156,11 @@ def _keep_for(stream, device, *tensors):
             t.record_stream(side)
 
 
+def _new(like, shape, dtype, stream):
+    make = lambda: like.new_empty(shape, dtype=dtype)
+    return make() if stream is None else _empty_on(stream, like.get_device(), make)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
@@ -180,11 +190,13 @@ def w4a16_matmul(x, wq, scales, biases, y=None, stream=None):
     import torch
     M, N, K = _check_tensors(x, wq, scales, biases, y)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(x, (M, N), torch.bfloat16, stream)
     elif tuple(y.shape) != (M, N):
         raise ValueError("y must be [M, N]")
     _check(lib.w4a16_matmul(_ptr(x), _ptr(wq), _ptr(scales), _ptr(biases), _ptr(y), M, N, K,
                             _stream_handle(stream)), "w4a16_matmul")
+    if stream is not None:
+        _keep_for(stream, x.get_device(), x, wq, scales, biases, y)
     return y
 
 
@@ -198,12 +210,14 @@ def w4a16_matmul_ex(x, wq, scales, biases, y=None, stream=None, path=PATH_AUTO, 
     import torch
     M, N, K = _check_tensors(x, wq, scales, biases, y)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(x, (M, N), torch.bfloat16, stream)
     elif tuple(y.shape) != (M, N):
         raise ValueError("y must be [M, N]")
     opt = make_options(path, splits, workers, 0, flags, row_blocks)
     _check(lib.w4a16_matmul_ex(_ptr(x), _ptr(wq), _ptr(scales), _ptr(biases), _ptr(y), M, N, K,
                                _stream_handle(stream), ctypes.byref(opt)), "w4a16_matmul_ex")
+    if stream is not None:
+        _keep_for(stream, x.get_device(), x, wq, scales, biases, y)
     return y
 
 
@@ -213,12 +227,14 @@ def w4a16_matmul_last_rows(x, wq, scales, biases, keep: int, y=None, stream=None
     M, N, K = _check_tensors(x, wq, scales, biases, None)
     rows = M if keep == 0 else keep
     if y is None:
-        y = torch.empty((rows, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(x, (rows, N), torch.bfloat16, stream)
     elif tuple(y.shape) != (rows, N):
         raise ValueError("y must be [keep, N]")
     _check(lib.w4a16_matmul_last_rows(_ptr(x), _ptr(wq), _ptr(scales), _ptr(biases), _ptr(y), M,
                                       int(keep), N, K, _stream_handle(stream)),
            "w4a16_matmul_last_rows")
+    if stream is not None:
+        _keep_for(stream, x.get_device(), x, wq, scales, biases, y)
     return y
 
 
@@ -234,6 +250,8 @@ def w4a16_matvec_noalloc(x, wq, scales, biases, y, stream=None):
         raise ValueError("y must be [M, N]")
     _check(lib.w4a16_matvec_noalloc(_ptr(x), _ptr(wq), _ptr(scales), _ptr(biases), _ptr(y), M, N, K,
                                     _stream_handle(stream)), "w4a16_matvec_noalloc")
+    if stream is not None:
+        _keep_for(stream, x.get_device(), x, wq, scales, biases, y)
     return y
 
 
@@ -256,11 +274,13 @@ def w4a16_gate_up(x, wq, scales, biases, h=None, stream=None):
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
     N2 = N // 2
     if h is None:
-        h = torch.empty((M, N2), dtype=torch.bfloat16, device=x.device)
+        h = _new(x, (M, N2), torch.bfloat16, stream)
     elif tuple(h.shape) != (M, N2):
         raise ValueError("h must be [M, N2]")
     _check(lib.w4a16_gate_up(_ptr(x), _ptr(wq), _ptr(scales), _ptr(biases), _ptr(h), M, N2, K,
                              _stream_handle(stream)), "w4a16_gate_up")
+    if stream is not None:
+        _keep_for(stream, x.get_device(), x, wq, scales, biases, h)
     return h
 
 
@@ -284,11 +304,13 @@ def w4a16_matmul_bits(x, wq, scales, biases, bits: int, y=None, stream=None):
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, wq {tuple(wq.shape)}, "
                          f"scales {tuple(scales.shape)}, biases {tuple(biases.shape)} for {bits}-bit codes")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(x, (M, N), torch.bfloat16, stream)
     elif tuple(y.shape) != (M, N) or y.dtype != torch.bfloat16 or not y.is_cuda or not y.is_contiguous():
         raise ValueError("y must be a contiguous bfloat16 CUDA tensor [M, N]")
     _check(lib.w4a16_matmul_bits(_ptr(x), _ptr(wq), _ptr(scales), _ptr(biases), _ptr(y), M, N, K, int(bits),
                                  _stream_handle(stream)), "w4a16_matmul_bits")
+    if stream is not None:
+        _keep_for(stream, x.get_device(), x, wq, scales, biases, y)
     return y
 
 
@@ -308,15 +330,17 @@ def w4a16_quantize(w, wq=None, scales=None, biases=None, stream=None):
     if K % 128:
         raise W4A16Error(ERR_UNSUPPORTED, "w4a16_quantize")
     if wq is None:
-        wq = torch.empty((N, K // 8), dtype=torch.int32, device=w.device)
+        wq = _new(w, (N, K // 8), torch.int32, stream)
     if scales is None:
-        scales = torch.empty((N, K // 128), dtype=torch.bfloat16, device=w.device)
+        scales = _new(w, (N, K // 128), torch.bfloat16, stream)
     if biases is None:
-        biases = torch.empty((N, K // 128), dtype=torch.bfloat16, device=w.device)
+        biases = _new(w, (N, K // 128), torch.bfloat16, stream)
     if tuple(wq.shape) != (N, K // 8) or tuple(scales.shape) != (N, K // 128) or tuple(biases.shape) != (N, K // 128):
         raise ValueError("output shapes must be [N, K/8], [N, K/128], [N, K/128]")
     _check(lib.w4a16_quantize(_ptr(w), dt, _ptr(wq), _ptr(scales), _ptr(biases), N, K, _stream_handle(stream)),
            "w4a16_quantize")
+    if stream is not None:
+        _keep_for(stream, w.get_device(), w, wq, scales, biases)
     return wq, scales, biases
 
 
@@ -324,11 +348,8 @@ def w4a16_quantize(w, wq=None, scales=None, biases=None, stream=None):
 #
 # wq int32/uint32 [N, K/8] codes and scales uint8 [N, K/32], as in include/w4a16.h.  Tensors are
 # contiguous and on one CUDA device, which need not be the current one; outputs that are not given
-# are allocated there.  With `stream`, the work runs on that stream, behind what is on it alone: the
-# caller orders it behind the work that makes the inputs, and uses of the outputs behind it.  New outputs
-# are then that stream's memory, and every tensor of the call may be dropped before its work is done.  A
-# decode loop runs these functions for every token, so each looks at what it was given in one expression,
-# and only a call that fails it goes on to find out why.
+# are allocated there.  A decode loop runs these functions for every token, so each looks at what it
+# was given in one expression, and only a call that fails it goes on to find out why.
 
 MX_BLOCK = 32
 

@@ -61,7 +61,8 @@ def fake(monkeypatch):
     class Library:
         def __getattr__(self, name):
             def call(*args):
-                Streams.calls.append((name, args[-1]))
+                stream = args[-2] if name == "w4a16_matmul_ex" else args[-1]
+                Streams.calls.append((name, getattr(stream, "value", stream)))
                 return 0
             call.__name__ = name
             return call
@@ -84,14 +85,32 @@ def mx_calls(**kw):
     }
 
 
+def affine_calls(**kw):
+    x, w = Fake.make(2, 128), Fake.make(16, 128)
+    wq, s, b = Fake.make(16, 16, dtype=torch.int32), Fake.make(16, 1), Fake.make(16, 1)
+    wq8 = Fake.make(16, 32, dtype=torch.int32)
+    return {
+        "affine matmul": ((x, wq, s, b), lambda: w4.w4a16_matmul(x, wq, s, b, **kw)),
+        "affine matmul_ex": ((x, wq, s, b), lambda: w4.w4a16_matmul_ex(x, wq, s, b, **kw)),
+        "affine last_rows": ((x, wq, s, b), lambda: w4.w4a16_matmul_last_rows(x, wq, s, b, 1, **kw)),
+        "affine gate_up": ((x, wq, s, b), lambda: w4.w4a16_gate_up(x, wq, s, b, **kw)),
+        "affine bits": ((x, wq8, s, b), lambda: w4.w4a16_matmul_bits(x, wq8, s, b, 8, **kw)),
+        "affine quantize": ((w,), lambda: w4.w4a16_quantize(w, **kw)),
+    }
+
+
+def calls(**kw):
+    return {**mx_calls(**kw), **affine_calls(**kw)}
+
+
 def outputs(result):
     return result if isinstance(result, tuple) else (result,)
 
 
-@pytest.mark.parametrize("name", list(mx_calls()))
+@pytest.mark.parametrize("name", list(calls()))
 @pytest.mark.parametrize("given", [Stream(9), 9], ids=["stream", "handle"])
 def test_outputs_on_a_given_stream(fake, name, given):
-    inputs, call = mx_calls(stream=given)[name]
+    inputs, call = calls(stream=given)[name]
     for out in outputs(call()):
         assert out.owner == 9                                    # its memory is the given stream's
         assert (out.data_ptr(), 7) in Streams.recorded           # and the current stream may use it
@@ -100,9 +119,9 @@ def test_outputs_on_a_given_stream(fake, name, given):
     assert [stream for _, stream in Streams.calls] == [9] and Streams.current == 7
 
 
-@pytest.mark.parametrize("name", list(mx_calls()))
+@pytest.mark.parametrize("name", list(calls()))
 @pytest.mark.parametrize("given", [None, Stream(7), 7], ids=["none", "stream", "handle"])
 def test_outputs_on_the_current_stream(fake, name, given):
-    _, call = mx_calls(stream=given)[name]
+    _, call = calls(stream=given)[name]
     assert all(out.owner == 7 for out in outputs(call()))
     assert not Streams.recorded and [stream for _, stream in Streams.calls] == [7]

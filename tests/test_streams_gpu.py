@@ -14,14 +14,22 @@ M, N, K = 40, 512, 1024
 BUSY = 20_000_000                      # clock cycles, some 10 ms
 
 
-def mx_calls():
+def calls():
     g = torch.Generator(device="cuda")
     g.manual_seed(5)
     normal = lambda r, c: torch.randn(r, c, generator=g, device="cuda").bfloat16()
     x, dy, dh, w = normal(M, K), normal(M, N), normal(M, N // 2), normal(N, K)
     wq, s = w4.w4a16_mx_quantize(w)
     xq, xs = w4.w4a16_mx_quantize(x)
+    layer = w4.w4a16_quantize(w)
+    codes8 = torch.randint(-2 ** 31, 2 ** 31 - 1, (N, K // 4), generator=g, device="cuda", dtype=torch.int32)
     return {
+        "affine quantize": (w4.w4a16_quantize, (w,)),
+        "affine matmul": (w4.w4a16_matmul, (x, *layer)),
+        "affine matmul_ex": (lambda *a, **kw: w4.w4a16_matmul_ex(*a, path=w4.PATH_GEMM, **kw), (x, *layer)),
+        "affine last_rows": (lambda *a, **kw: w4.w4a16_matmul_last_rows(*a, 3, **kw), (x, *layer)),
+        "affine gate_up": (w4.w4a16_gate_up, (x[:5], *layer)),
+        "affine bits": (lambda *a, **kw: w4.w4a16_matmul_bits(*a, 8, **kw), (x[:20], codes8, *layer[1:])),
         "quantize": (w4.w4a16_mx_quantize, (x,)),
         "dequantize": (w4.w4a16_mx_dequantize, (wq, s)),
         "matmul": (w4.w4a16_mx_matmul, (x, wq, s)),
@@ -32,14 +40,19 @@ def mx_calls():
     }
 
 
-NAMES = ["quantize", "dequantize", "matmul", "matmul_a4", "gate_up", "matmul_backward", "gate_up_backward"]
+NAMES = ["quantize", "dequantize", "matmul", "matmul_a4", "gate_up", "matmul_backward", "gate_up_backward",
+         "affine quantize", "affine matmul", "affine matmul_ex", "affine last_rows", "affine gate_up", "affine bits"]
 
 
 def every(name):
-    call, args = mx_calls()[name]
+    call, args = calls()[name]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call(*args)                                            # a first call, which may set a workspace up
+    torch.cuda.synchronize()
     want = call(*args)
     torch.cuda.synchronize()
-    return call, args, want if isinstance(want, tuple) else (want,)
+    return side, call, args, want if isinstance(want, tuple) else (want,)
 
 
 def tuple_of(result):
@@ -54,8 +67,7 @@ def equal(got, want):
 @pytest.mark.parametrize("handle", [False, True])
 @pytest.mark.parametrize("name", NAMES)
 def test_outputs_beside_pending_work_on_freed_memory(name, handle):
-    call, args, want = every(name)
-    side = torch.cuda.Stream()
+    side, call, args, want = every(name)
     victims = [torch.full_like(w, 3) for w in want]            # memory of the outputs' sizes
     torch.cuda.synchronize()
     torch.cuda._sleep(BUSY)
@@ -71,8 +83,7 @@ def test_outputs_beside_pending_work_on_freed_memory(name, handle):
 
 @pytest.mark.parametrize("name", NAMES)
 def test_inputs_dropped_after_the_call(name):
-    call, args, want = every(name)
-    side = torch.cuda.Stream()
+    side, call, args, want = every(name)
     mine = [a.clone() for a in args]
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
@@ -88,8 +99,7 @@ def test_inputs_dropped_after_the_call(name):
 
 @pytest.mark.parametrize("name", NAMES)
 def test_outputs_dropped_while_the_current_stream_reads_them(name):
-    call, args, want = every(name)
-    side = torch.cuda.Stream()
+    side, call, args, want = every(name)
     got = tuple_of(call(*args, stream=side))
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda._sleep(BUSY)

@@ -350,6 +350,10 @@ def w4a16_quantize(w, wq=None, scales=None, biases=None, stream=None):
 # contiguous and on one CUDA device, which need not be the current one; outputs that are not given
 # are allocated there.  A decode loop runs these functions for every token, so each looks at what it
 # was given in one expression, and only a call that fails it goes on to find out why.
+#
+# The C functions take scales that start on 16 bytes, which rows cut out of a larger array (a shard, the
+# last token of a quantised prompt) seldom do, as a row has K/32 of them.  Such scales are copied first, by
+# every call: a program that uses them often clones them once.  Scales to be written have to be aligned.
 
 MX_BLOCK = 32
 
@@ -430,6 +434,15 @@ def _mx_out(name, t, like, dtype, rows, cols, device, stream):
     return t
 
 
+def _mx_aligned(scales, device, stream):
+    """A copy, on the call's stream, of scales that do not start on 16 bytes."""
+    side = None if stream is None else _side_stream(stream, device)
+    if side is None:
+        return scales.clone()
+    with _torch.cuda.stream(side):
+        return scales.clone()
+
+
 def _mx_run(fn, device, stream, *args):
     """Calls a C entry point on `device`, made current for the call, and its stream."""
     if stream is None:
@@ -473,7 +486,8 @@ def w4a16_mx_dequantize(wq, scales, w=None, dtype=None, stream=None):
     if dtype is not _f32 and dtype is not _bf16:
         raise TypeError("values come in float32 or bfloat16")
     w = _mx_out("w", w, wq, dtype, N, K, device, stream)
-    _mx_run(lib.w4a16_mx_dequantize, device, stream, wq.data_ptr(), scales.data_ptr(), w.data_ptr(),
+    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
+    _mx_run(lib.w4a16_mx_dequantize, device, stream, wq.data_ptr(), ws.data_ptr(), w.data_ptr(),
             DTYPE_F32 if dtype is _f32 else DTYPE_BF16, N, K)
     if stream is not None:
         _keep_for(stream, device, wq, scales, w)
@@ -485,7 +499,8 @@ def w4a16_mx_matmul(x, wq, scales, y=None, stream=None):
     M, K, device = _mx_rows("x", x)
     N = _mx_stored(wq, scales, K, device)[0]
     y = _mx_out("y", y, x, _bf16, M, N, device, stream)
-    _mx_run(lib.w4a16_mx_matmul, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K)
+    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
+    _mx_run(lib.w4a16_mx_matmul, device, stream, x.data_ptr(), wq.data_ptr(), ws.data_ptr(), y.data_ptr(), M, N, K)
     if stream is not None:
         _keep_for(stream, device, x, wq, scales, y)
     return y
@@ -496,7 +511,9 @@ def w4a16_mx_matmul_a4(xq, xscales, wq, scales, y=None, stream=None):
     M, K, device = _mx_stored(xq, xscales, None, None, ("xq", "xscales"))
     N = _mx_stored(wq, scales, K, device)[0]
     y = _mx_out("y", y, xq, _bf16, M, N, device, stream)
-    _mx_run(lib.w4a16_mx_matmul_a4, device, stream, xq.data_ptr(), xscales.data_ptr(), wq.data_ptr(), scales.data_ptr(),
+    xs = xscales if xscales.data_ptr() & 15 == 0 else _mx_aligned(xscales, device, stream)
+    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
+    _mx_run(lib.w4a16_mx_matmul_a4, device, stream, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
             y.data_ptr(), M, N, K)
     if stream is not None:
         _keep_for(stream, device, xq, xscales, wq, scales, y)
@@ -511,7 +528,8 @@ def w4a16_mx_gate_up(x, wq, scales, h=None, stream=None):
     if N % 16:
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
     h = _mx_out("h", h, x, _bf16, M, N // 2, device, stream)
-    _mx_run(lib.w4a16_mx_gate_up, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), h.data_ptr(), M, N // 2, K)
+    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
+    _mx_run(lib.w4a16_mx_gate_up, device, stream, x.data_ptr(), wq.data_ptr(), ws.data_ptr(), h.data_ptr(), M, N // 2, K)
     if stream is not None:
         _keep_for(stream, device, x, wq, scales, h)
     return h
@@ -526,7 +544,8 @@ def w4a16_mx_matmul_backward(dy, wq, scales, dx=None, stream=None):
     if rows != N:
         raise ValueError(f"dy has {N} columns, W {rows} rows")
     dx = _mx_out("dx", dx, dy, _bf16, M, K, device, stream)
-    _mx_run(lib.w4a16_mx_matmul_backward, device, stream, dy.data_ptr(), wq.data_ptr(), scales.data_ptr(), dx.data_ptr(),
+    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
+    _mx_run(lib.w4a16_mx_matmul_backward, device, stream, dy.data_ptr(), wq.data_ptr(), ws.data_ptr(), dx.data_ptr(),
             M, N, K)
     if stream is not None:
         _keep_for(stream, device, dy, wq, scales, dx)
@@ -544,7 +563,8 @@ def w4a16_mx_gate_up_backward(x, wq, scales, dh, dx=None, dgu=None, stream=None)
         _mx_refuse("dh", dh, (_bf16,), (M, N // 2), device)
     dx = _mx_out("dx", dx, x, _bf16, M, K, device, stream)
     dgu = _mx_out("dgu", dgu, x, _bf16, M, N, device, stream)
-    _mx_run(lib.w4a16_mx_gate_up_backward, device, stream, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), dh.data_ptr(),
+    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
+    _mx_run(lib.w4a16_mx_gate_up_backward, device, stream, x.data_ptr(), wq.data_ptr(), ws.data_ptr(), dh.data_ptr(),
             dgu.data_ptr(), dx.data_ptr(), M, N // 2, K)
     if stream is not None:
         _keep_for(stream, device, x, wq, scales, dh, dx, dgu)

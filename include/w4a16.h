@@ -318,7 +318,10 @@ int w4a16_matmul_bits(const void *x, const uint32_t *wq, const void *scales,
  * negatives.
  *   wq      uint32 [N, K/8]    code of w[n,k]: (wq[n*(K/8) + k/8] >> (4*(k%8))) & 15
  *   scales  uint8  [N, K/32]
- * Every pointer must be 16-byte aligned.  Activations and gradients are BF16, row-major, contiguous.
+ * Every pointer must be 16-byte aligned, the scales' too: the tensor-core kernels fetch them in words and
+ * chunks at such addresses, of which none but the last may reach beyond the array.  (Rows cut out of a
+ * larger array seldom start there: copy their scales, as the Python binding does.)  Activations and
+ * gradients are BF16, row-major, contiguous.
  * K must be a multiple of 32 and sizes below 2^31 - 65536 (else W4A16_ERR_UNSUPPORTED); negative
  * sizes, null pointers with non-empty sizes and an output that overlaps another buffer are
  * W4A16_ERR_INVALID_ARG.  An empty output launches nothing; an empty sum is +0.  Nothing behind the

@@ -254,5 +254,23 @@ __device__ __forceinline__ void gated_backward(float g, float u, float dh, float
     du = dh * (g * s);
 }
 
+// Both gradients where the sums are empty, g = u = 0: zeros, but not a number where dh is not finite.
+// dh and dgu by eights: dh's block i is followed by dgu's blocks 2 i (gate) and 2 i + 1 (up).
+__global__ void __launch_bounds__(kQThreads) empty_gates_kernel(const uint4 *dh, uint4 *dgu, long long blocks) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long stride = static_cast<long long>(gridDim.x) * kQThreads;
+    for (long long i = static_cast<long long>(blockIdx.x) * kQThreads + threadIdx.x; i < blocks; i += stride) {
+        const uint4 d = ldg_v4(dh + i);
+        const float v[8] = {bf16_lo_to_f32(d.x), bf16_hi_to_f32(d.x), bf16_lo_to_f32(d.y), bf16_hi_to_f32(d.y),
+                            bf16_lo_to_f32(d.z), bf16_hi_to_f32(d.z), bf16_lo_to_f32(d.w), bf16_hi_to_f32(d.w)};
+        float a[8], b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gated_backward(0.f, 0.f, v[j], a[j], b[j]);
+        dgu[2 * i] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+        dgu[2 * i + 1] = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]), pack_bf16x2(b[6], b[7]));
+    }
+}
+
 }  // namespace mx
 }  // namespace w4a16

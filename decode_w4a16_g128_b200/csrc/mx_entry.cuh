@@ -485,7 +485,12 @@ int w4a16_mx_gate_up_backward(const void *x, const uint32_t *wq, const uint8_t *
     rc = mx_device(&d);
     if (rc) return rc;
     if (N2 == 0) return K == 0 ? W4A16_OK : zero_fill(dx, s[0].bytes, stream);
-    if (K == 0) return zero_fill(dgu, s[1].bytes, stream);   // g = u = 0: both gradients are 0
+    if (K == 0) {
+        const long long blocks = M * (N2 / 8);
+        const dim3 grid(stream_grid(blocks, 1, d->sms), 1, 1);
+        return mx_launch(mx::empty_gates_kernel, grid, 1, mx::kQThreads, 0, stream, static_cast<const uint4 *>(dh),
+                         static_cast<uint4 *>(dgu), blocks);
+    }
     rc = mx_gemm(d, x, wq, scales, dh, dgu, M, 2 * N2, K, 2 * N2, K, false, mxg::kGatedBackward, stream);
     if (rc) return rc;
     return mx_gemm(d, dgu, wq, scales, nullptr, dx, M, K, 2 * N2, 2 * N2, K, true, mxg::kPlain, stream);

@@ -280,11 +280,28 @@ int mx_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *
     return mx_launch(mx4::a4_kernel, grid, 2, mx4::kThreads, mx4::kSmemBytes, stream, tx, tw, ty, p);
 }
 
-// Few rows of x take the matvec: up to 16 always, up to 32 where the weight is small.  Measured, us,
-// matvec / GEMM: M = 16 N x K 9728 x 2560 11.1 / 13.2, 2560 x 9728 15.1 / 16.5; M = 32 1024 x 2560
-// 6.7 / 9.4, 4096 x 2560 8.9 / 10.8, but 2560 x 9728 26.7 / 16.5 and 19456 x 2560 38 / 22.4.
-bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
-    return M <= 16 || (M <= mxv::kMaxM && N * K <= (int64_t(1) << 24));
+// Few rows of x take the row kernel: up to 8 always; up to 16 where the weight times the rows beyond 8 is not
+// large and K not long, as every CTA of 16 weight rows reads all of x from the cache, group by group, nor long
+// for CTAs of four warps that leave SMs half empty; up to 32 where K is short and every CTA of eight warps is
+// resident.  Measured, us, row kernel / GEMM, N x K, weights from HBM:
+//   M = 8   9728 x 2560 8.6 / 13.0, 151936 x 2560 77.7 / 94.4, 2560 x 19456 20.5 / 22.7; but 16384 x 16384
+//           73.8 / 68.6, 5120 x 9728 24.4 / 21.1, 512 x 65536 34.8 / 30.4
+//   M = 9   19456 x 2560 16.0 / 21.3, 38912 x 2560 27.8 / 31.6, 9728 x 9728 32.6 / 36.8; but 12800 x 5120
+//           24.9 / 21.8, and not taken: 5120 x 9728 29.7 / 21.1, 1024 x 12288 15.2 / 14.0, 512 x 65536 58.3 / 30.5
+//   M = 12  9728 x 2560 10.2 / 13.1, 38912 x 2560 30.8 / 31.5, 9728 x 9728 34.1 / 36.8; but 12800 x 2560
+//           15.3 / 13.4, and not taken: 151936 x 2560 101.7 / 94.6, 1024 x 16384 20.3 / 15.8
+//   M = 16  9728 x 2560 11.6 / 13.1, 4096 x 9728 16.5 / 18.3, 19456 x 2560 21.3 / 21.4; but 12800 x 2560
+//           18.4 / 13.3, and not taken: 38912 x 2560 38.0 / 31.7, 151936 x 2560 123.9 / 94.6
+//   M = 17  1024 x 2560 6.9 / 9.1, 4096 x 4096 9.9 / 12.8; not taken: 6400 x 2560 12.6 / 11.7, 1024 x 8192
+//           16.0 / 12.9
+//   M = 32  1024 x 2560 8.5 / 9.1, 4096 x 2560 8.8 / 10.6, 4096 x 4096 13.1 / 12.8; not taken: 2560 x 9728
+//           26.9 / 16.3
+bool mx_few_rows(int64_t M, int64_t N, int64_t K, int sms) {
+    if (M <= 8) return true;
+    const int64_t blocks = (N + 15) / 16;
+    if (M > 16) return M <= mxv::kMaxM && K <= 4096 && blocks <= 2 * sms;
+    if (K > 4096 && blocks > 2 * sms && blocks < 4 * sms) return false;
+    return K < 12288 && (M - 8) * N <= (int64_t(3) << 27) / K;
 }
 
 template <int NB, int WARPS, int D, int CTAS, bool X4>
@@ -411,7 +428,7 @@ int w4a16_mx_matmul(const void *x, const uint32_t *wq, const uint8_t *scales, vo
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(y, s[0].bytes, stream);   // an empty sum
-    if (mx_few_rows(M, N, K)) return mx_matvec(d, x, wq, scales, y, M, N, K, false, stream);
+    if (mx_few_rows(M, N, K, d->sms)) return mx_matvec(d, x, wq, scales, y, M, N, K, false, stream);
     return mx_gemm(d, x, wq, scales, nullptr, y, M, N, K, N, K, false, mxg::kPlain, stream);
 }
 
@@ -447,7 +464,7 @@ int w4a16_mx_gate_up(const void *x, const uint32_t *wq, const uint8_t *scales, v
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(h, s[0].bytes, stream);   // silu(0) 0 = +0
-    if (mx_few_rows(M, 2 * N2, K)) return mx_matvec(d, x, wq, scales, h, M, 2 * N2, K, true, stream);
+    if (mx_few_rows(M, 2 * N2, K, d->sms)) return mx_matvec(d, x, wq, scales, h, M, 2 * N2, K, true, stream);
     return mx_gemm(d, x, wq, scales, nullptr, h, M, 2 * N2, K, 2 * N2, K, false, mxg::kGated, stream);
 }
 

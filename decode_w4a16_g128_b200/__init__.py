@@ -133,17 +133,18 @@ def _side_stream(stream, device):
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device)
 
 
-def _empty_on(stream, device, make):
-    """A new output, make(), for work on a stream that was given.  Memory of the current stream would not
-    do: what it hands out may be memory that was freed there with work in front of it still pending, which
-    the given stream does not wait for.  So the block comes from the given stream's memory, and is not
-    reused there before the current stream, on which the caller may use it, has come past its end."""
+def _empty_on(stream, device, like, shape, dtype):
+    """A new output for work on a stream that was given, on the device of `like`.  Memory of the current
+    stream would not do: what it hands out may be memory that was freed there with work in front of it
+    still pending, which the given stream does not wait for.  So the block comes from the given stream's
+    memory, and is not reused there before the current stream, on which the caller may use it, has come
+    past its end."""
     import torch
     side = _side_stream(stream, device)
     if side is None:
-        return make()
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(side):
-        t = make()
+        t = like.new_empty(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream(device))
     return t
 
@@ -157,8 +158,9 @@ def _keep_for(stream, device, *tensors):
 
 
 def _new(like, shape, dtype, stream):
-    make = lambda: like.new_empty(shape, dtype=dtype)
-    return make() if stream is None else _empty_on(stream, like.get_device(), make)
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _empty_on(stream, like.get_device(), like, shape, dtype)
 
 
 def _ptr(t):
@@ -427,7 +429,7 @@ def _mx_out(name, t, like, dtype, rows, cols, device, stream):
         if stream is None:
             t = like.new_empty((rows, cols)) if dtype is like.dtype else like.new_empty((rows, cols), dtype=dtype)
         else:
-            t = _empty_on(stream, device, lambda: like.new_empty((rows, cols), dtype=dtype))
+            t = _empty_on(stream, device, like, (rows, cols), dtype)
     elif not (isinstance(t, _Tensor) and (_mx_ok(t, dtype, rows, cols, device) or (
             dtype is _i32 and _mx_ok(t, _u32, rows, cols, device)))):
         _mx_refuse(name, t, (_i32, _u32) if dtype is _i32 else (dtype,), (rows, cols), device)
@@ -486,8 +488,11 @@ def w4a16_mx_dequantize(wq, scales, w=None, dtype=None, stream=None):
     if dtype is not _f32 and dtype is not _bf16:
         raise TypeError("values come in float32 or bfloat16")
     w = _mx_out("w", w, wq, dtype, N, K, device, stream)
-    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
-    _mx_run(lib.w4a16_mx_dequantize, device, stream, wq.data_ptr(), ws.data_ptr(), w.data_ptr(),
+    ws = scales.data_ptr()
+    if ws & 15:
+        copy = _mx_aligned(scales, device, stream)
+        ws = copy.data_ptr()
+    _mx_run(lib.w4a16_mx_dequantize, device, stream, wq.data_ptr(), ws, w.data_ptr(),
             DTYPE_F32 if dtype is _f32 else DTYPE_BF16, N, K)
     if stream is not None:
         _keep_for(stream, device, wq, scales, w)
@@ -499,8 +504,11 @@ def w4a16_mx_matmul(x, wq, scales, y=None, stream=None):
     M, K, device = _mx_rows("x", x)
     N = _mx_stored(wq, scales, K, device)[0]
     y = _mx_out("y", y, x, _bf16, M, N, device, stream)
-    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
-    _mx_run(lib.w4a16_mx_matmul, device, stream, x.data_ptr(), wq.data_ptr(), ws.data_ptr(), y.data_ptr(), M, N, K)
+    ws = scales.data_ptr()
+    if ws & 15:
+        copy = _mx_aligned(scales, device, stream)
+        ws = copy.data_ptr()
+    _mx_run(lib.w4a16_mx_matmul, device, stream, x.data_ptr(), wq.data_ptr(), ws, y.data_ptr(), M, N, K)
     if stream is not None:
         _keep_for(stream, device, x, wq, scales, y)
     return y
@@ -511,9 +519,15 @@ def w4a16_mx_matmul_a4(xq, xscales, wq, scales, y=None, stream=None):
     M, K, device = _mx_stored(xq, xscales, None, None, ("xq", "xscales"))
     N = _mx_stored(wq, scales, K, device)[0]
     y = _mx_out("y", y, xq, _bf16, M, N, device, stream)
-    xs = xscales if xscales.data_ptr() & 15 == 0 else _mx_aligned(xscales, device, stream)
-    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
-    _mx_run(lib.w4a16_mx_matmul_a4, device, stream, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+    xs = xscales.data_ptr()
+    if xs & 15:
+        xcopy = _mx_aligned(xscales, device, stream)
+        xs = xcopy.data_ptr()
+    ws = scales.data_ptr()
+    if ws & 15:
+        copy = _mx_aligned(scales, device, stream)
+        ws = copy.data_ptr()
+    _mx_run(lib.w4a16_mx_matmul_a4, device, stream, xq.data_ptr(), xs, wq.data_ptr(), ws,
             y.data_ptr(), M, N, K)
     if stream is not None:
         _keep_for(stream, device, xq, xscales, wq, scales, y)
@@ -528,8 +542,11 @@ def w4a16_mx_gate_up(x, wq, scales, h=None, stream=None):
     if N % 16:
         raise ValueError("the interleaved gate/up rows come in blocks of 16")
     h = _mx_out("h", h, x, _bf16, M, N // 2, device, stream)
-    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
-    _mx_run(lib.w4a16_mx_gate_up, device, stream, x.data_ptr(), wq.data_ptr(), ws.data_ptr(), h.data_ptr(), M, N // 2, K)
+    ws = scales.data_ptr()
+    if ws & 15:
+        copy = _mx_aligned(scales, device, stream)
+        ws = copy.data_ptr()
+    _mx_run(lib.w4a16_mx_gate_up, device, stream, x.data_ptr(), wq.data_ptr(), ws, h.data_ptr(), M, N // 2, K)
     if stream is not None:
         _keep_for(stream, device, x, wq, scales, h)
     return h
@@ -544,8 +561,11 @@ def w4a16_mx_matmul_backward(dy, wq, scales, dx=None, stream=None):
     if rows != N:
         raise ValueError(f"dy has {N} columns, W {rows} rows")
     dx = _mx_out("dx", dx, dy, _bf16, M, K, device, stream)
-    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
-    _mx_run(lib.w4a16_mx_matmul_backward, device, stream, dy.data_ptr(), wq.data_ptr(), ws.data_ptr(), dx.data_ptr(),
+    ws = scales.data_ptr()
+    if ws & 15:
+        copy = _mx_aligned(scales, device, stream)
+        ws = copy.data_ptr()
+    _mx_run(lib.w4a16_mx_matmul_backward, device, stream, dy.data_ptr(), wq.data_ptr(), ws, dx.data_ptr(),
             M, N, K)
     if stream is not None:
         _keep_for(stream, device, dy, wq, scales, dx)
@@ -563,8 +583,11 @@ def w4a16_mx_gate_up_backward(x, wq, scales, dh, dx=None, dgu=None, stream=None)
         _mx_refuse("dh", dh, (_bf16,), (M, N // 2), device)
     dx = _mx_out("dx", dx, x, _bf16, M, K, device, stream)
     dgu = _mx_out("dgu", dgu, x, _bf16, M, N, device, stream)
-    ws = scales if scales.data_ptr() & 15 == 0 else _mx_aligned(scales, device, stream)
-    _mx_run(lib.w4a16_mx_gate_up_backward, device, stream, x.data_ptr(), wq.data_ptr(), ws.data_ptr(), dh.data_ptr(),
+    ws = scales.data_ptr()
+    if ws & 15:
+        copy = _mx_aligned(scales, device, stream)
+        ws = copy.data_ptr()
+    _mx_run(lib.w4a16_mx_gate_up_backward, device, stream, x.data_ptr(), wq.data_ptr(), ws, dh.data_ptr(),
             dgu.data_ptr(), dx.data_ptr(), M, N // 2, K)
     if stream is not None:
         _keep_for(stream, device, x, wq, scales, dh, dx, dgu)

@@ -5,7 +5,8 @@
 //
 // Mathematics: a stored value code 2^(e - 127) has two significant bits, so it is exact in BF16 (the
 // scale is applied before the product, no factor is left for the accumulator) and the tensor cores'
-// products are exact in FP32; the sum over all of the contraction stays in tensor memory.
+// products are exact in FP32 (within its normal range); the sum over all of the contraction stays in tensor
+// memory.
 //
 // A CTA pair (cta_group::2) computes 256 rows x BN <= 256 outputs, K = 128 of the contraction a stage:
 //   A  128 rows of x per CTA, by TMA, K-major, two tiles of 64 k with the 128-byte swizzle;
@@ -27,10 +28,10 @@
 // waiter is a whole ring behind what it waits for: a team's next stage is in the same slot, so it has
 // waited for this one's MMAs, and the parities never alias.
 //
-// Bound, forward, 2048 x 9728 x 2560: 71.2 us (1.43 PFLOP/s; the tensor pipe is active 73 % of the time, the
-// integer pipe 44 %, issue slots 48 %, DRAM 4 %).  What is left is the time between two stages' MMAs: with
+// Bound, forward, 2048 x 9728 x 2560: 72.2 us (1.41 PFLOP/s; the tensor pipe is active 71 % of the time, the
+// integer pipe 43 %, issue slots 47 %, DRAM 4 %).  What is left is the time between two stages' MMAs: with
 // stages of K = 64, whose MMAs take less time than the instructions around a stage's waits do in a crowded
-// SM, the same product took 84 us.  Backward, 2048 x 9728 x 2560: 72.8 us (1.40 PFLOP/s), of which the shared
+// SM, the same product took 84 us.  Backward, 2048 x 9728 x 2560: 73.4 us (1.39 PFLOP/s), of which the shared
 // last tiles save 8.  Few rows (33 - 128 x 9728 x 2560): 13.3 us: a stage is as long as its codes take to
 // expand, three at a time, each a chain of waits.
 #pragma once

@@ -2,7 +2,8 @@
 // interleaved in blocks of eight.
 //
 // Mathematics: the codes become BF16 with their scale applied, exactly, so that mma.sync m16n8k16 (codes
-// as A: 16 weight rows x 16 k; x as B: 16 k x 8 rows of x) sums exact products in FP32 over all of K.
+// as A: 16 weight rows x 16 k; x as B: 16 k x 8 rows of x) sums products in FP32 over all of K, each exact
+// within FP32's normal range.
 //
 // Lane (g, t) = (lane / 4, lane % 4) owns block 4 c + t of rows g and g + 8 in the c-th group of 128 k:
 // one 16-byte load and one scale byte a row, so a block's factor is one register.  A permutation of k
@@ -16,8 +17,9 @@
 // all CTAs of an SM read, is taken from its cache when it is needed (with x fetched ahead too, there are
 // registers for two groups: 8 rows x 9728 x 2560 8.2 us, 7.6 so).  Every CTA is resident at once at a decode
 // layer's sizes.
-// Bound: one row x 9728 x 2560 (13 MB) takes 7.0 us where its bytes take 2.0: launch, first loads and the
-// join are half of it, and the expanding keeps the integer pipe half busy (tensor pipe 11 %, DRAM 14 %).
+// Bound: one row x 9728 x 2560 (13 MB from HBM) takes 8.1 us where its bytes take 2.0: launch, the first
+// loads, which wait for the preceding kernel, and the join are half of it, and the expanding keeps the
+// integer pipe half busy (tensor pipe 10 %, DRAM 14 %).
 #pragma once
 
 #include "mx.cuh"

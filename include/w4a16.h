@@ -327,8 +327,9 @@ int w4a16_matmul_bits(const void *x, const uint32_t *wq, const void *scales,
  * W4A16_ERR_INVALID_ARG.  An empty output launches nothing; an empty sum is +0.  Nothing behind the
  * last row is read or written.
  *
- * Numerics: every stored value is exact in BF16, every product exact in FP32; sums are FP32 (order
- * fixed by the sizes and the device model, so results repeat bit for bit), rounded once to BF16.
+ * Numerics: every stored value is exact in BF16, every product exact in FP32 as long as it lies in FP32's
+ * normal range; sums are FP32 (order fixed by the sizes and the device model, so results repeat bit for
+ * bit), rounded once to BF16.
  * Values of 2^128 and more (from e = 253 on; the quantiser ends at 252) are infinities; only
  * w4a16_mx_matmul_a4 may also take them as they are.
  * NaN and infinities in a row of x reach that row's outputs alone; a NaN block of W reaches its
@@ -336,7 +337,8 @@ int w4a16_matmul_bits(const void *x, const uint32_t *wq, const void *scales,
  *
  * Execution: on `stream` of the current device, without waiting, allocating or using a library
  * workspace: the calls may be captured without a warm-up call, and calls on different streams or
- * replays of different graphs share nothing.
+ * replays of different graphs share nothing.  A kernel may begin before the preceding one has ended, but
+ * reads and writes nothing before that one's writes are visible: inputs may come from any work in front.
  */
 
 /*

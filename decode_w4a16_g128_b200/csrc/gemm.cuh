@@ -476,14 +476,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t r[32];
                 if (i >= nbs) {
                     // chunks 2 half, 2 half + 1 (words 8 half .. 8 half + 7) of this row's codes
-                    if (!mbar_wait(&w_full[cs.slot], cs.phase)) { ok = false; break; }
+                    if (!mbar_wait_warp(&w_full[cs.slot], cs.phase)) { ok = false; break; }
                     const uint32_t wrow = smem_u32(smem + kOffW + cs.slot * kWBytes) + rl * 64;
                     const uint4 c0 = lds128(wrow + (((2u * half) ^ sw) << 4));
                     const uint4 c1 = lds128(wrow + (((2u * half + 1u) ^ sw) << 4));
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&w_empty[cs.slot]);   // the codes are in registers
                     cs.advance();
-                    if (g >= kABufs && !mbar_wait(&done[fs.slot], fs.phase)) { ok = false; break; }
+                    if (g >= kABufs && !mbar_wait_warp(&done[fs.slot], fs.phase)) { ok = false; break; }
                     tc_fence_after();   // the tensor cores' reads of this buffer precede the stores below
                     const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int jj = 0; jj < 8; ++jj)
                         v[jj] = row_ok ? ldg_v4(bcrow + t * 16 + half * 8 + jj) : make_uint4(0, 0, 0, 0);
-                    if (g >= kABufs && !mbar_wait(&done[fs.slot], fs.phase)) { ok = false; break; }
+                    if (g >= kABufs && !mbar_wait_warp(&done[fs.slot], fs.phase)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll
                     for (int jj = 0; jj < 8; ++jj) {
@@ -549,14 +549,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool row_ok = row < p.N;
             const int sb = nsb == 2 ? (k & 1) : 0;
             const uint32_t use = static_cast<uint32_t>(nsb == 2 ? (k >> 1) : k);
-            if (ok && !mbar_wait(&sc_full[sb], use & 1u)) ok = false;   // this tile's scales are staged
+            if (ok && !mbar_wait_warp(&sc_full[sb], use & 1u)) ok = false;   // this tile's scales are staged
             const uint16_t *srow = sc_smem + sb * BN * G + nl * G;
             unsigned long long acc2[32];   // FP32 pairs: x rows 2j, 2j + 1 of this warp's 64
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc2[j] = 0ull;
             for (int i = 0; i < steps && ok; ++i) {
                 const float sc = (row_ok && i >= nbs) ? 0.125f * bf16_to_f32(srow[g0 + i - nbs]) : 1.f;   // s / 8
-                if (!mbar_wait(&done[ds.slot], ds.phase)) { ok = false; break; }
+                if (!mbar_wait_warp(&done[ds.slot], ds.phase)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t r[64];
                 tmem_ld64(taddr + db * BM, r);

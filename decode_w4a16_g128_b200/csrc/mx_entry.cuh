@@ -346,11 +346,12 @@ int mx_matvec(DeviceInfo *d, const void *x, const uint32_t *wq, const uint8_t *w
     return mx_matvec_launch<4, 8, 1, 2, false>(p, stream);
 }
 
-// The same with x in 4 bits, for up to 8 rows and all but the largest weights: past that the FP4 tensor
-// cores are faster, as here x is expanded anew for every 16 weight rows.  Measured, us, this / FP4 tensor
-// cores: N x K 1024 x 2560 M = 1 4.7 / 8.4, 4096 x 2560 M = 8 5.8 / 9.0, 9728 x 2560 M = 8 9.7 / 10.6, 2560 x
-// 9728 M = 8 13.1 / 16.6, 19456 x 2560 M = 4 14.7 / 14.8, but 9728 x 9728 M = 8 31.3 / 23.5.
-bool mx_few_a4(int64_t M, int64_t N, int64_t K) { return M <= 8 && N * K <= (int64_t(1) << 26); }
+// The same with x in 4 bits, for up to 8 rows where every CTA is resident with eight warps or more, or K is
+// short: else the FP4 tensor cores are faster, as here x is expanded anew for every 16 weight rows.  Measured,
+// us, this / FP4 tensor cores, M = 8, N x K, weights from HBM: 1024 x 2560 3.9 / 6.4, 4736 x 2560 4.9 / 8.4,
+// 4096 x 9728 12.7 / 15.2, 512 x 65536 37.4 / 71.5, 9728 x 1024 4.6 / 6.7, 151936 x 512 25.4 / 30.3; not taken:
+// 4752 x 2560 8.5 / 7.3, 9728 x 2560 9.2 / 8.8, 5120 x 9728 25.9 / 15.8, 151936 x 2560 84.1 / 52.6.
+bool mx_few_a4(int64_t M, int64_t N, int64_t K, int sms) { return M <= 8 && ((N + 15) / 16 <= 2 * sms || K <= 1536); }
 
 int mx_matvec_a4(DeviceInfo *d, const uint32_t *xq, const uint8_t *xs, const uint32_t *wq, const uint8_t *ws, void *out,
                  int64_t M, int64_t N, int64_t K, void *stream) {
@@ -445,7 +446,7 @@ int w4a16_mx_matmul_a4(const uint32_t *xq, const uint8_t *xscales, const uint32_
     rc = mx_device(&d);
     if (rc) return rc;
     if (K == 0) return zero_fill(y, s[0].bytes, stream);
-    if (mx_few_a4(M, N, K)) return mx_matvec_a4(d, xq, xscales, wq, scales, y, M, N, K, stream);
+    if (mx_few_a4(M, N, K, d->sms)) return mx_matvec_a4(d, xq, xscales, wq, scales, y, M, N, K, stream);
     return mx_a4(d, xq, xscales, wq, scales, y, M, N, K, stream);
 }
 

@@ -40,3 +40,37 @@ def test_products_on_both_sides(M, N, K):
     want = (xd @ w.T).float().bfloat16()
     assert torch.equal(y, want)
     assert (buf[:lo] == 7).all() and (buf[lo + M * N:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [1, 8, 9])
+@pytest.mark.parametrize("N,K", [(4736, 1568), (4737, 1536), (4737, 1568), (9728, 2560), (33, 32768), (151, 9728)])
+def test_4_bit_products_on_both_sides(M, N, K):
+    rng = np.random.default_rng([51, M, N, K])
+    wq, s, w = stored(rng, N, K)
+    xq, xs, x = stored(rng, M, K)
+    xs -= 3
+    x = x / 8
+    # products are multiples of 1/128, and no sum of them, in whatever order, reaches 2^24 of these
+    assert float((x.abs() @ w.abs().T).max()) * 128 < 2 ** 24
+    want = (x @ w.T).float().bfloat16()
+    assert torch.equal(w4.w4a16_mx_matmul_a4(xq, xs, wq, s), want)
+
+
+def test_long_rows_of_4_bit_values_on_the_tensor_cores():
+    """Rows of 2^27 values, more of them than the row kernel takes: codes at a few places, zeros between."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    M, N, K = 9, 4, 2 ** 27
+    rng = np.random.default_rng(52)
+    at = [0, 39, K // 2 + 8, K - 40, K - 1]
+    px, pw = rng.integers(0, 16, (M, len(at))), rng.integers(0, 16, (N, len(at)))
+
+    def spread(picked):
+        wq = torch.zeros(picked.shape[0], K // 8, dtype=torch.int32, device="cuda")
+        nibbles = picked.astype(np.uint32) << np.array([4 * (i % 8) for i in at], np.uint32)
+        wq[:, [i // 8 for i in at]] = torch.from_numpy(nibbles.view(np.int32)).cuda()
+        return wq, torch.full((picked.shape[0], K // 32), 127, dtype=torch.uint8, device="cuda")
+
+    y = w4.w4a16_mx_matmul_a4(*spread(px), *spread(pw)).double().cpu().numpy()
+    assert np.array_equal(y, ref.bf16(ref.GRID[px] @ ref.GRID[pw].T))
+    assert w4.w4a16_device_status() == w4.OK

@@ -128,8 +128,12 @@ def _side_stream(stream, device):
     """A stream that was given as torch's, or None where it is the device's current one."""
     import torch
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == 1:                    # the other name of the default stream, which torch calls 0
+        handle = 0
     if handle == torch._C._cuda_getCurrentRawStream(device):
         return None
+    if handle == 0:                    # for torch a stream without a handle is a new one
+        return torch.cuda.default_stream(device)
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device)
 
 

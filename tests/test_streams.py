@@ -54,7 +54,8 @@ def fake(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch.cuda, "stream", use)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(Streams.current))
-    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle or 99))   # 0: a new one
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: Streams.current, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
 
@@ -125,3 +126,15 @@ def test_outputs_on_the_current_stream(fake, name, given):
     _, call = calls(stream=given)[name]
     assert all(out.owner == 7 for out in outputs(call()))
     assert not Streams.recorded and [stream for _, stream in Streams.calls] == [7]
+
+
+@pytest.mark.parametrize("name", list(calls()))
+@pytest.mark.parametrize("given", [0, 1])
+def test_outputs_on_the_default_stream_by_its_handle(fake, name, given):
+    inputs, call = calls(stream=given)[name]
+    for out in outputs(call()):
+        assert out.owner == 0 and (out.data_ptr(), 7) in Streams.recorded
+    for t in inputs:
+        assert (t.data_ptr(), 0) in Streams.recorded
+    Streams.current, Streams.recorded = 0, []
+    assert all(out.owner == 0 for out in outputs(call())) and not Streams.recorded

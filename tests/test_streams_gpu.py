@@ -111,3 +111,17 @@ def test_outputs_dropped_while_the_current_stream_reads_them(name):
     torch.cuda.synchronize()
     equal(kept, want)
     assert all((o == 1).all() for o in others)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_default_stream_by_its_handle(name):
+    """stream=0 from within another current stream: work in order with the default stream's."""
+    side, call, args, want = every(name)
+    torch.cuda._sleep(BUSY)                                    # on the default stream
+    victims = [torch.full_like(w, 3) for w in want]
+    with torch.cuda.stream(side):
+        got = tuple_of(call(*args, stream=0))
+    kept = [v.clone() for v in victims]
+    torch.cuda.synchronize()
+    equal(got, want)
+    assert all((k == 3).all() for k in kept)
